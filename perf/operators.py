@@ -13,13 +13,16 @@ The plain forms below state what each computes:
   logprob = x_t - lse;  H = -sum p log p;  a token outside [0, M) leaves its row out (zeros, (-inf, -1), not read)
   d/dx_v = g_lp ([v = t] - p_v) - g_H p_v (log p_v + H)
   list entries count where the id is in [0, M) and the value is above -inf; a row without one is left out
-  plain: q = softmax of the listed values / T;  rest: q = exp(values), q_r = max(0, 1 - sum q)
+  plain: q = softmax of the listed values / T;  rest: q = exp(values), q_r = 1 - sum q, 0 where that is below 2^-20
+  (what the rounding of fp32 log probabilities can leave of a full list)
   loss = sum q_k (log q_k - log p_k) [+ q_r (log q_r - log p_r), p_r the mass of the unlisted columns]
 """
 import numpy as np
 import torch
 
 own = False
+
+LEAST_REST = 2.0 ** -20
 
 TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
 
@@ -203,7 +206,8 @@ def _plain_distil(s):
         er = (dr - mr).exp()
         zr = er.sum(1, keepdim=True, dtype=torch.float64)
         logp_r = torch.where(some, zr.log() + mr.double() - ls, 0.0)
-        q_r = torch.where(some & kept, (1.0 - q.sum(1, keepdim=True)).clamp_min(0.0), 0.0)
+        q_r = 1.0 - q.sum(1, keepdim=True)
+        q_r = torch.where(some & kept & (q_r >= LEAST_REST), q_r, 0.0)
         logq = torch.where(valid, values, 0.0)
     else:
         y = values / T
@@ -318,7 +322,7 @@ def exact(case, seed):
         p = x.sub_(lse[:, None]).exp_().mul_(total[:, None])
         p.index_put_((r, v), -q, accumulate=True)
         return {"loss": loss, "grad": p.mul_((w / T)[:, None])}
-    q_r = torch.where(kept, (1 - total).clamp(min=0), 0.0)
+    q_r = torch.where(kept & (1 - total >= LEAST_REST), 1 - total, 0.0)
     at_list = x[r, v]
     x[r, v] = -np.inf
     R = torch.logsumexp(x, 1)
