@@ -1,4 +1,4 @@
-"""ctypes binding of libtp's C ABI (include/tp.h): the same names, argument marshalling only.
+"""ctypes binding of libtp's C ABI (include/tp.h, include/tp_logits.h): the same names, argument marshalling only.
 
 Loading fails loudly when ``libtp.so`` has not been built: there is no fallback of any kind.
 """
@@ -12,6 +12,7 @@ import threading
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libtp.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "tp.h")
+LOGITS_HEADER = os.path.join(os.path.dirname(PKG), "include", "tp_logits.h")
 
 TP_OK, TP_ERR_INVALID_ARG, TP_ERR_UNSUPPORTED, TP_ERR_CUDA, TP_ERR_WORKSPACE, TP_ERR_TIMEOUT = range(6)
 TP_F32, TP_F64 = 0, 1
@@ -35,12 +36,22 @@ class tp_pairs(ctypes.Structure):
                 ("X", ctypes.c_void_p), ("Y", ctypes.c_void_p)]
 
 
+class tp_rows(ctypes.Structure):
+    """Stored score rows (include/tp_logits.h)."""
+    _fields_ = [("dtype", ctypes.c_int), ("N", ctypes.c_int64), ("M", ctypes.c_int64), ("group", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64), ("group_stride", ctypes.c_int64), ("data", ctypes.c_void_p)]
+
+
+TP_ROWS_F32, TP_ROWS_F16, TP_ROWS_BF16 = 0, 1, 2
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
 _INT = ctypes.c_int
 _PAIRS = ctypes.POINTER(tp_pairs)
 _SCORE = ctypes.POINTER(tp_score)
+_ROWS = ctypes.POINTER(tp_rows)
+_F64 = ctypes.c_double
 
 SIGNATURES = {
     "tp_pairwise_matmul": ([_PAIRS, _SCORE, _P, _I64, _P, _P, _SZ, _P], _INT),
@@ -69,6 +80,15 @@ SIGNATURES = {
     "tp_selftest_exp64": ([_P, _P, _I64, _P], _INT),
 }
 
+# include/tp_logits.h: consumers of stored score rows
+LOGITS_SIGNATURES = {
+    "tp_token_logprobs": ([_ROWS, _P, _F64, _INT, _P, _P, _P, _P, _P, _P], _INT),
+    "tp_token_logprobs_backward": ([_ROWS, _P, _F64, _P, _P, _P, _ROWS, _P], _INT),
+    "tp_topk_distillation": ([_ROWS, _INT, _P, _P, _F64, _INT, _P, _P, _P], _INT),
+    "tp_topk_distillation_backward": ([_ROWS, _INT, _P, _P, _F64, _INT, _P, _P, _ROWS, _P], _INT),
+    "tp_topk_distillation_grad": ([_ROWS, _INT, _P, _P, _P, _F64, _INT, _P, _P, _ROWS, _P], _INT),
+}
+
 LAUNCH_HOOK = ctypes.CFUNCTYPE(None, ctypes.c_char_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p)
 
 _lock = threading.Lock()
@@ -81,9 +101,9 @@ class TPError(RuntimeError):
         super().__init__(f"{where}: {detail}")
 
 
-def header_symbols() -> list[str]:
-    """Every function the public header declares."""
-    text = open(HEADER).read()
+def header_symbols(path: str = HEADER) -> list[str]:
+    """Every function a public header declares."""
+    text = open(path).read()
     return sorted(set(re.findall(r"^TP_API\s+[\w\s\*]+?\b(tp_\w+)\s*\(", text, flags=re.M)))
 
 
@@ -98,7 +118,7 @@ def load(path: str | None = None):
             raise ImportError(f"libtp is not built ({p} missing): run `python -m lazy_score_matrix_gb300.build` "
                               "or __graft_entry__.build(); there is no CPU fallback")
         lib = ctypes.CDLL(p)
-        for name, (args, res) in SIGNATURES.items():
+        for name, (args, res) in {**SIGNATURES, **LOGITS_SIGNATURES}.items():
             f = getattr(lib, name)
             f.argtypes = args
             f.restype = res
@@ -123,6 +143,6 @@ def launch_count(reset: bool = False) -> int:
 
 
 def __getattr__(name):
-    if name in SIGNATURES:
+    if name in SIGNATURES or name in LOGITS_SIGNATURES:
         return getattr(load(), name)
     raise AttributeError(name)

@@ -1,8 +1,12 @@
-"""Build libtp.so in-tree: every csrc/*.cu compiled for sm_103a in parallel, then linked.
+"""Build libtp.so in-tree: every csrc/*.cu and csrc_logits/*.cu compiled for sm_103a in parallel, then linked.
 
 Usage: ``python -m lazy_score_matrix_gb300.build`` (or ``__graft_entry__.build()``).
 Objects go to ``lazy_score_matrix_gb300/_build/``; the library to ``lazy_score_matrix_gb300/libtp.so``.
-A translation unit is recompiled when it or any header in csrc/ or include/ is newer than its object.
+A translation unit is recompiled when it or any header in csrc/, csrc_logits/ or include/ is newer than its object.
+
+csrc/ holds the consumers of lazy scores (include/tp.h), csrc_logits/ those of stored score rows
+(include/tp_logits.h). They are apart because the recorded traffic and instruction counts of the lazy
+consumers' benchmark are keyed to a hash of csrc/ and tp.h (bench.py, source_hash).
 """
 from __future__ import annotations
 
@@ -16,6 +20,7 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
+CSRC_LOGITS = os.path.join(PKG, "csrc_logits")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtp.so")
@@ -25,7 +30,7 @@ PEAKS_LIB = os.path.join(PKG, "libtp_peaks.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
-              "-I" + INCLUDE, "-I" + CSRC]
+              "-I" + INCLUDE, "-I" + CSRC, "-I" + CSRC_LOGITS]
 
 
 def nvcc() -> str:
@@ -36,8 +41,7 @@ def nvcc() -> str:
 
 
 def _headers_mtime() -> float:
-    hs = glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        glob.glob(os.path.join(INCLUDE, "*.h"))
+    hs = [h for d in (CSRC, CSRC_LOGITS, INCLUDE) for h in glob.glob(os.path.join(d, "*.h")) + glob.glob(os.path.join(d, "*.cuh"))]
     return max(os.path.getmtime(h) for h in hs)
 
 
@@ -50,7 +54,7 @@ def _compile(src: str, extra: list[str]) -> tuple[str, int, str]:
 
 def build(force: bool = False, jobs: int | None = None, verbose: bool = False, extra: list[str] | None = None) -> str:
     os.makedirs(OBJ_DIR, exist_ok=True)
-    srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu"))) + sorted(glob.glob(os.path.join(CSRC_LOGITS, "*.cu")))
     hdr = _headers_mtime()
     todo = []
     for s in srcs:

@@ -1,0 +1,66 @@
+// Kernel arguments of the stored-row consumers (include/tp_logits.h), shared by the C entries and the
+// kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "tp_logits.h"
+
+namespace tp {
+namespace rows {
+
+constexpr int kMaxList = 128;  // longest list of alternatives, and of a teacher's columns
+// The unlisted columns' share 1 - sum q counts as 0 below this: log probabilities rounded to fp32, and a common
+// error of their normaliser of a few 2^-24, leave up to about 1e-6 of a full list, and a student that masks
+// everything else by a large negative score would turn such a remainder into any loss at all.
+constexpr double kLeastRest = 1.0 / (1 << 20);
+constexpr int kStats = 8;      // floats per row that a forward leaves for its backward
+
+struct View {
+    void* data;
+    int64_t row_stride, group_stride;
+    int M, group;
+};
+
+// The temperature as the kernels use it: c = log2(e)/T rounded to fp32 (exponents are 2^(c d)), inv = 1/T, and
+// delta = 1/T - c ln 2, what the rounding of c takes from the exponent's slope: a sum s of exponentials
+// with first moment h is corrected to s + delta h.
+struct Scale {
+    float c, delta, inv;
+    double inv64;
+};
+
+struct LogprobArgs {
+    View x;
+    int64_t N;
+    const int64_t* tokens;
+    Scale sc;
+    int top;
+    float *logprobs, *entropy, *stats, *top_logprobs;
+    int64_t* top_ids;
+    // backward
+    const float *g_logprob, *g_entropy;
+    View g;
+};
+
+struct DistillArgs {
+    View x;
+    int64_t N;
+    const int64_t* ids;
+    const float* values;
+    int K, rest;
+    Scale sc;
+    float *loss, *stats;
+    // backward
+    const float* weights;
+    View g;
+};
+
+void launch_logprobs(tp_rows_dtype t, const LogprobArgs& a, cudaStream_t s);
+void launch_logprobs_backward(tp_rows_dtype t, const LogprobArgs& a, cudaStream_t s);
+void launch_distill(tp_rows_dtype t, const DistillArgs& a, cudaStream_t s);
+void launch_distill_backward(tp_rows_dtype t, const DistillArgs& a, cudaStream_t s);
+
+}  // namespace rows
+}  // namespace tp
