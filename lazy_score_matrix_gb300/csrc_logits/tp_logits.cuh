@@ -18,6 +18,8 @@
 namespace tp {
 namespace rows {
 
+constexpr int kThreads = 256;  // per CTA of every kernel here
+constexpr int kUnroll = 4;     // 16-byte vectors a thread has in flight
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr double kLn2 = 0.69314718055994530942;
 
@@ -37,6 +39,9 @@ struct Elem<float> {
     static constexpr int kVec = 4;  // elements of a 16-byte vector
     __device__ __forceinline__ static float get(float v) { return v; }
     __device__ __forceinline__ static float put(float v) { return v; }
+    __device__ __forceinline__ static uint4 pack(const float* f) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
     __device__ __forceinline__ static void unpack(const uint4& v, float* f) {
         f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
     }
@@ -46,6 +51,13 @@ struct Elem<__half> {
     static constexpr int kVec = 8;
     __device__ __forceinline__ static float get(__half v) { return __half2float(v); }
     __device__ __forceinline__ static __half put(float v) { return __float2half_rn(v); }
+    __device__ __forceinline__ static uint32_t two(float a, float b) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    __device__ __forceinline__ static uint4 pack(const float* f) {
+        return make_uint4(two(f[0], f[1]), two(f[2], f[3]), two(f[4], f[5]), two(f[6], f[7]));
+    }
     __device__ __forceinline__ static void pair(uint32_t u, float* f) {
         const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&u));
         f[0] = r.x, f[1] = r.y;
@@ -59,6 +71,13 @@ struct Elem<__nv_bfloat16> {
     static constexpr int kVec = 8;
     __device__ __forceinline__ static float get(__nv_bfloat16 v) { return __bfloat162float(v); }
     __device__ __forceinline__ static __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
+    __device__ __forceinline__ static uint32_t two(float a, float b) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    __device__ __forceinline__ static uint4 pack(const float* f) {
+        return make_uint4(two(f[0], f[1]), two(f[2], f[3]), two(f[4], f[5]), two(f[6], f[7]));
+    }
     __device__ __forceinline__ static void pair(uint32_t u, float* f) {
         f[0] = __uint_as_float(u << 16), f[1] = __uint_as_float(u & 0xffff0000u);
     }
@@ -86,14 +105,71 @@ struct RowVecs {
         n = (int)(((int64_t)M + off + V - 1) / V);
     }
     __device__ __forceinline__ int64_t first(int j) const { return (int64_t)j * V - off; }
+    // vectors j0 .. j1 - 1 all lie inside the row
     __device__ __forceinline__ bool inside(int j0, int j1) const { return first(j0) >= 0 && first(j1) <= M; }
-    __device__ __forceinline__ uint4 raw(int j) const { return __ldg(reinterpret_cast<const uint4*>(p + first(j))); }
+    __device__ __forceinline__ const uint4* at(int j) const { return reinterpret_cast<const uint4*>(p + first(j)); }
+    __device__ __forceinline__ uint4 raw(int j) const { return __ldg(at(j)); }
     __device__ __forceinline__ void edge(int j, float* f) const {
         const int64_t e = first(j);
 #pragma unroll
         for (int i = 0; i < V; ++i) f[i] = (j < n && e + i >= 0 && e + i < M) ? Elem<T>::get(p[e + i]) : neg_inf();
     }
 };
+
+// 16 bytes from byte `shift` (0 .. 15, a multiple of 2) of the 32 bytes (a, b).
+__device__ __forceinline__ uint4 window(const uint4& a, const uint4& b, int shift) {
+    uint32_t w0 = a.x, w1 = a.y, w2 = a.z, w3 = a.w, w4 = b.x, w5 = b.y;
+    if (shift & 8) w0 = a.z, w1 = a.w, w2 = b.x, w3 = b.y, w4 = b.z, w5 = b.w;
+    if (shift & 4) w0 = w1, w1 = w2, w2 = w3, w3 = w4, w4 = w5;
+    const int r = (shift & 2) * 8;
+    return make_uint4(__funnelshift_r(w0, w1, r), __funnelshift_r(w1, w2, r), __funnelshift_r(w2, w3, r), __funnelshift_r(w3, w4, r));
+}
+
+// The threads that share a row: a warp (several rows a CTA), or the CTA. kThreads threads a CTA either way.
+template <int TEAM>
+struct Team {
+    static constexpr int kPerCta = kThreads / TEAM;
+    static constexpr bool kWarp = TEAM == 32;
+    __device__ __forceinline__ static int id() { return kWarp ? threadIdx.x >> 5 : 0; }
+    __device__ __forceinline__ static int tid() { return kWarp ? threadIdx.x & 31 : threadIdx.x; }
+    __device__ __forceinline__ static void sync() {
+        if (kWarp) __syncwarp();
+        else __syncthreads();
+    }
+    __device__ __forceinline__ static bool any(bool v) { return kWarp ? __any_sync(~0u, v) : __syncthreads_or(v); }
+    __device__ __forceinline__ static int count(bool v) { return kWarp ? __popc(__ballot_sync(~0u, v)) : __syncthreads_count(v); }
+};
+
+// Thread-block clusters: the CTAs of a cluster share one row, rank r the r-th slice of its vectors.
+__device__ __forceinline__ int cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return (int)r;
+}
+__device__ __forceinline__ int cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return (int)r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// the same shared-memory object in the CTA of another rank
+template <class P>
+__device__ __forceinline__ P* of_rank(P* p, int rank) {
+    uint64_t a;
+    asm("mapa.u64 %0, %1, %2;" : "=l"(a) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
+    return reinterpret_cast<P*>(a);
+}
+
+struct Slice {
+    int begin, end;  // vectors of the row
+};
+__device__ __forceinline__ Slice slice_of(int n, int rank, int parts) {
+    const int per = (n + parts - 1) / parts;
+    Slice s;
+    s.begin = min(n, rank * per), s.end = min(n, s.begin + per);
+    return s;
+}
 
 // Order of fp32 values as unsigned integers (-inf lowest); +0 and -0 are one value.
 __device__ __forceinline__ uint32_t ord_of(float v) {
@@ -170,16 +246,21 @@ __device__ __forceinline__ void warp_sum(State& st) {
 }
 
 struct ReduceBuf {
-    float m[32], s[32], lo[32], h[32];
+    float m[kThreads / 32], s[kThreads / 32], lo[kThreads / 32], h[kThreads / 32];
 };
 
-// The state of all scores of the CTA, in every thread. Uses two barriers; the buffer may be used again
-// after the caller's next barrier.
-template <int TPB>
-__device__ __forceinline__ State block_state(State st, float c, ReduceBuf& b) {
-    constexpr int W = TPB / 32;
+// The state of all scores of the team, in every thread. A CTA's takes two barriers; the buffer may be used
+// again after the caller's next one.
+template <int TEAM>
+__device__ __forceinline__ State team_state(State st, float c, ReduceBuf& b) {
+    constexpr int W = TEAM / 32;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const float wm = warp_max(st.m);
+    if (W == 1) {
+        st.raise(wm, c);
+        warp_sum(st);
+        return st;
+    }
     if (lane == 0) b.m[w] = wm;
     __syncthreads();
     const float m = warp_max(b.m[lane < W ? lane : 0]);
@@ -190,6 +271,30 @@ __device__ __forceinline__ State block_state(State st, float c, ReduceBuf& b) {
     st.s = lane < W ? b.s[lane] : 0.f, st.lo = lane < W ? b.lo[lane] : 0.f, st.h = lane < W ? b.h[lane] : 0.f;
     warp_sum(st);
     return st;
+}
+
+constexpr int kMaxCluster = 8;
+struct ClusterBuf {
+    float4 part[kMaxCluster];
+};
+// Every CTA's state to every CTA of the cluster; the caller then crosses a cluster barrier and merges.
+__device__ __forceinline__ void cluster_share(const State& st, ClusterBuf& b, int rank, int size) {
+    if ((int)threadIdx.x < size) of_rank(&b, threadIdx.x)->part[rank] = make_float4(st.m, st.s, st.lo, st.h);
+}
+__device__ __forceinline__ State cluster_merge(const ClusterBuf& b, int size, float c) {
+    float m = b.part[0].x;
+    for (int r = 1; r < size; ++r) m = max_nan(m, b.part[r].x);
+    State all;
+    all.m = m;
+    for (int r = 0; r < size; ++r) {
+        const float4 v = b.part[r];
+        State p;
+        p.m = v.x, p.s = v.y, p.lo = v.z, p.h = v.w;
+        p.raise(m, c);
+        all.add(p.s);
+        all.lo += p.lo, all.h += p.h;
+    }
+    return all;
 }
 
 // c is rounded: the sum's first-order correction to the exact 1/T (see Scale in tp_logits_args.h)
@@ -215,32 +320,127 @@ __device__ __forceinline__ double warp_sum64(double v) {
 struct ListBuf {
     int id[kMaxList];
     float y[kMaxList], x[kMaxList];  // the teacher's value, the row's score
-    unsigned char ok[kMaxList];      // the entry counts
+    float q[kMaxList];               // the teacher's share
     unsigned char first[kMaxList];   // no earlier entry has its column
+    __device__ __forceinline__ bool ok(int k) const { return id[k] >= 0; }
 };
 
-// Loads the list of a row whose scores start at p; false when no entry counts. Ends with a barrier.
-template <class T, int TPB>
-__device__ __forceinline__ bool load_list(const DistillArgs& a, int64_t row, const T* p, ListBuf& l) {
+// Loads the list of a row whose scores start at p; false when no entry counts. Scores are read of the columns
+// from e0 to e1 only (what another CTA may be overwriting is its own to read). Ends with a barrier.
+template <class T, int TEAM>
+__device__ __forceinline__ bool load_list(const DistillArgs& a, int64_t row, const T* p, ListBuf& l, int64_t e0, int64_t e1) {
     bool some = false;
-    for (int k = threadIdx.x; k < a.K; k += TPB) {
+    for (int k = Team<TEAM>::tid(); k < a.K; k += TEAM) {
         const int64_t id = a.ids[row * a.K + k];
         const float y = a.values[row * a.K + k];
         const bool ok = id >= 0 && id < a.x.M && !(y == neg_inf());
         l.id[k] = ok ? (int)id : -1;
         l.y[k] = y;
-        l.ok[k] = ok;
-        l.x[k] = ok ? Elem<T>::get(p[id]) : 0.f;
+        l.x[k] = ok && id >= e0 && id < e1 ? Elem<T>::get(p[id]) : 0.f;
         some |= ok;
     }
-    if (!__syncthreads_or(some)) return false;
-    for (int k = threadIdx.x; k < a.K; k += TPB) {
+    if (!Team<TEAM>::any(some)) return false;
+    Team<TEAM>::sync();
+    return true;
+}
+// Marks the first entry of each column; true when a column is listed twice. Ends with a barrier.
+template <int TEAM>
+__device__ __forceinline__ bool mark_first(ListBuf& l, int K) {
+    bool twice = false;
+    for (int k = Team<TEAM>::tid(); k < K; k += TEAM) {
         bool first = true;
         for (int j = 0; j < k; ++j) first &= l.id[j] != l.id[k];
         l.first[k] = first;
+        twice |= !first && l.ok(k);
     }
-    __syncthreads();
-    return true;
+    twice = Team<TEAM>::any(twice);
+    Team<TEAM>::sync();
+    return twice;
+}
+
+struct RowStats {
+    float loss;
+    float m, ls;    // maximum and log of the sum relative to it, over all columns
+    float gm, gls;  // the same over the columns that the list leaves (rest), else over all
+    float Z;        // sum of the shares
+    float coef;     // gradient of a column that is not listed: coef exp((x - gm)/T - gls) / T
+};
+
+// The list's part of a row, by one warp: the teacher's shares q (left in l.q), the loss, and what the gradient
+// takes. `st` is the state of all columns, or of the unlisted ones (rest; l.first and every l.x are then
+// read). In fp64: what is left of a loss near zero is the difference of logarithms that agree to several digits.
+__device__ __forceinline__ RowStats distill_row(const DistillArgs& a, const State& st, ListBuf& l) {
+    const int lane = threadIdx.x & 31;
+    const double inv = a.sc.inv64;
+    const double zs = exact_sum(st, a.sc);
+    float m = st.m;  // maximum over all columns
+    double z = zs;   // sum over all columns, relative to m
+    double q[4], lq[4];
+    if (a.rest) {
+        float lm = neg_inf();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int k = lane + 32 * j;
+            if (k < a.K && l.ok(k)) lm = max_nan(lm, l.x[k]);
+        }
+        m = max_nan(st.m, warp_max(lm));
+        double sum = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int k = lane + 32 * j;
+            const bool ok = k < a.K && l.ok(k);
+            lq[j] = ok ? l.y[k] : 0.0;
+            q[j] = ok ? exp_table(lq[j]) : 0.0;
+            if (ok && l.first[k] && l.x[k] > neg_inf()) sum += exp_table(((double)l.x[k] - m) * inv);
+        }
+        z = warp_sum64(sum);
+        if (st.m > neg_inf()) z += zs * exp_table(((double)st.m - m) * inv);
+        if (m != m) z = m;  // NaN
+    } else {
+        float ym = neg_inf();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int k = lane + 32 * j;
+            if (k < a.K && l.ok(k)) ym = max_nan(ym, l.y[k]);
+        }
+        ym = warp_max(ym);
+        double sum = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int k = lane + 32 * j;
+            const bool ok = k < a.K && l.ok(k);
+            lq[j] = ok ? ((double)l.y[k] - ym) * inv : 0.0;
+            q[j] = ok ? exp_table(lq[j]) : 0.0;
+            sum += q[j];
+        }
+        sum = warp_sum64(sum);
+        const double ln = ln64(sum), r = 1.0 / sum;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] *= r, lq[j] -= ln;
+    }
+    const double m0 = m == neg_inf() ? 0.0 : (double)m, ls = m == neg_inf() ? 0.0 : ln64(z);
+    double loss = 0, Z = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int k = lane + 32 * j;
+        if (q[j] > 0) loss += q[j] * (lq[j] - (((double)l.x[k] - m0) * inv - ls));
+        Z += q[j];
+        if (k < a.K) l.q[k] = (float)q[j];
+    }
+    loss = warp_sum64(loss), Z = warp_sum64(Z);
+    RowStats s;
+    s.m = s.gm = m, s.ls = s.gls = (float)ls, s.coef = (float)Z;
+    if (a.rest) {
+        s.coef = 0.f;
+        if (st.m != neg_inf()) {
+            const double q_r = 1.0 - Z >= kLeastRest ? 1.0 - Z : 0.0, lr = ln64(zs), lp = ((double)st.m - m0) * inv + lr - ls;
+            if (q_r > 0) loss += q_r * (ln64(q_r) - lp);
+            Z += q_r;
+            s.gm = st.m, s.gls = (float)lr, s.coef = (float)(Z * exp_table(lp) - q_r);
+        }
+    }
+    s.Z = (float)Z, s.loss = (float)loss;
+    return s;
 }
 
 }  // namespace rows

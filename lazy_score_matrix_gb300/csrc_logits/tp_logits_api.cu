@@ -297,7 +297,8 @@ tp_status tp_topk_distillation_grad(const tp_rows* x, int K, const int64_t* ids,
         a.weights = weights;
         a.g = view(grad);
         const cudaStream_t s = static_cast<cudaStream_t>(stream);
-        launch_distill(x->dtype, a, s);
+        if (launch_distill_grad(x->dtype, a, s)) return launched(1);
+        launch_distill(x->dtype, a, s);  // rows too long to stay on chip
         launch_distill_backward(x->dtype, a, s);
         return launched(2);
     });

@@ -57,9 +57,47 @@ struct DistillArgs {
     View g;
 };
 
+// How a kernel's threads are laid over the rows: one warp a row, one CTA, or a cluster of CTAs.
+struct Shape {
+    bool warp;
+    int cluster;
+    unsigned grid;
+    size_t smem = 0;
+};
+constexpr int64_t kWarpCols = 4096, kWarpRows = 152 * 8;
+constexpr int64_t kFewRows = 152 * 4;
+
+// Many rows: one CTA a row, or, where a row is short, one warp a row. Few rows: up to 8 CTAs a row, as long as a
+// CTA keeps a chunk of `chunk` columns of its own.
+inline Shape shape_of(int64_t N, int64_t M, bool warps, int64_t chunk) {
+    Shape s;
+    s.warp = warps && M <= kWarpCols && N >= kWarpRows;
+    s.cluster = 1;
+    while (!s.warp && s.cluster < 8 && N * s.cluster < kFewRows && M >= 2 * s.cluster * chunk) s.cluster *= 2;
+    s.grid = (unsigned)(s.warp ? (N + 7) / 8 : N * s.cluster);
+    return s;
+}
+
+template <class... KArgs, class... Args>
+inline void launch(void (*kernel)(KArgs...), const Shape& sh, cudaStream_t s, const Args&... a) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(sh.grid);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = sh.smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)sh.cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = sh.cluster > 1 ? 1 : 0;
+    cudaLaunchKernelEx(&cfg, kernel, a...);
+}
+
 void launch_logprobs(tp_rows_dtype t, const LogprobArgs& a, cudaStream_t s);
 void launch_logprobs_backward(tp_rows_dtype t, const LogprobArgs& a, cudaStream_t s);
 void launch_distill(tp_rows_dtype t, const DistillArgs& a, cudaStream_t s);
+bool launch_distill_grad(tp_rows_dtype t, const DistillArgs& a, cudaStream_t s);  // false: the rows do not fit
 void launch_distill_backward(tp_rows_dtype t, const DistillArgs& a, cudaStream_t s);
 
 }  // namespace rows

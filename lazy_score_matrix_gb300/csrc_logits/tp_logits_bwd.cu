@@ -4,92 +4,119 @@
 
 #include "tp_launch.h"
 #include "tp_logits.cuh"
+#include "tp_logits_out.cuh"
 
 namespace tp {
 namespace rows {
 namespace {
 
-constexpr int kThreads = 256;
-
+// The scores of a row in global memory, fetched for 16-byte vectors of the gradient's alignment.
 template <class T>
-__device__ __forceinline__ void zero_row(const View& g, int64_t row) {
-    T* o = row_at<T>(g, row);
-    for (int i = threadIdx.x; i < g.M; i += kThreads) o[i] = Elem<T>::put(0.f);
+struct FromRow {
+    static constexpr int V = Elem<T>::kVec;
+    const T* p;
+    int M;
+    bool match;  // the scores have the gradient's alignment
+    __device__ __forceinline__ FromRow(const T* p_, int M_, const T* o)
+        : p(p_), M(M_), match(((reinterpret_cast<uintptr_t>(p_) ^ reinterpret_cast<uintptr_t>(o)) & 15u) == 0) {}
+    // false: elements e .. e + V - 1 have to be fetched one by one
+    __device__ __forceinline__ bool get(int64_t e, uint4& v) const {
+        if (match) {
+            v = __ldcs(reinterpret_cast<const uint4*>(p + e));  // not .nc: the gradient may overwrite the scores
+            return true;
+        }
+        const int shift = (int)(reinterpret_cast<uintptr_t>(p + e) & 15u), back = shift / (int)sizeof(T);
+        if (e - back < 0 || e - back + 2 * V > M) return false;
+        const uint4* q = reinterpret_cast<const uint4*>(p + (e - back));
+        v = window(q[0], q[1], shift);  // neighbours read the same bytes: cached
+        return true;
+    }
+    __device__ __forceinline__ float one(int64_t e) const { return Elem<T>::get(p[e]); }
+};
+
+// Rows are visited from the last to the first: the forward has read the last ones most recently, and what of
+// them is left in the cache need not come from memory again.
+template <int TEAM>
+__device__ __forceinline__ int64_t row_of(int64_t N, int parts) {
+    const int64_t r = TEAM == 32 ? (int64_t)blockIdx.x * Team<TEAM>::kPerCta + Team<TEAM>::id() : blockIdx.x / parts;
+    return N - 1 - r;
 }
 
-template <class T>
-__global__ void __launch_bounds__(kThreads) logprobs_bwd_kernel(const LogprobArgs a) {
-    const int64_t row = blockIdx.x;
+template <class T, int TEAM, bool ENTROPY>
+__global__ void __launch_bounds__(kThreads) logprobs_bwd_kernel(const LogprobArgs a, int parts) {
+    const int64_t row = row_of<TEAM>(a.N, parts);
+    if (row < 0) return;
+    T* o = row_at<T>(a.g, row);
+    const Range r = range_of(o, a.x.M, TEAM == 32 ? 0 : blockIdx.x % parts, parts);
     const int64_t tok = a.tokens ? a.tokens[row] : 0;
     const float* st = a.stats + row * kStats;
     const float m = st[0], ls = st[1], H = st[2];
-    if (tok < 0 || tok >= a.x.M || m == neg_inf()) return zero_row<T>(a.g, row);
-    const T* x = row_at<const T>(a.x, row);
-    T* o = row_at<T>(a.g, row);
-    const float g1 = a.g_logprob && a.tokens ? a.g_logprob[row] : 0.f, g2 = a.g_entropy ? a.g_entropy[row] : 0.f;
-    const float ls2 = ls * kLog2e;
-    for (int i = threadIdx.x; i < a.x.M; i += kThreads) {
-        const float t = max_nan(fmaf(Elem<T>::get(x[i]) - m, a.sc.c, -ls2), -1e30f);  // log2 p
-        const float p = ex2(t);
-        float g = -p * fmaf(g2, fmaf(t, (float)kLn2, H), g1);
-        if (i == tok) g += g1;
-        o[i] = Elem<T>::put(g * a.sc.inv);
-    }
+    if (tok < 0 || tok >= a.x.M || m == neg_inf()) return zero_range<T, TEAM>(o, r.e0, r.e1);
+    const float g1 = a.g_logprob ? a.g_logprob[row] * a.sc.inv : 0.f;
+    const float g2 = ENTROPY ? a.g_entropy[row] * a.sc.inv : 0.f;
+    const float ls2 = ls * kLog2e, c = a.sc.c, gt = a.g_logprob ? g1 : 0.f;
+    const float b1 = fmaf(g2, H, g1), b2 = g2 * (float)kLn2;
+    const FromRow<T> x(row_at<const T>(a.x, row), a.x.M, o);
+    map_range<T, TEAM>(o, r.e0, r.e1, x, [&](float* f, int64_t e) {
+#pragma unroll
+        for (int i = 0; i < Elem<T>::kVec; ++i) {
+            float t = fmaf(f[i] - m, c, -ls2);  // log2 p
+            if (ENTROPY) t = max_nan(t, -1e30f);  // p = 0 times a finite log
+            f[i] = -ex2(t) * (ENTROPY ? fmaf(b2, t, b1) : g1);
+        }
+        if (tok >= e && tok < e + Elem<T>::kVec) {
+#pragma unroll
+            for (int i = 0; i < Elem<T>::kVec; ++i)
+                if (tok == e + i) f[i] += gt;
+        }
+    });
 }
 
-template <class T>
-__global__ void __launch_bounds__(kThreads) distill_bwd_kernel(const DistillArgs a) {
-    __shared__ ListBuf list;
-    __shared__ float q[kMaxList];
-    const int64_t row = blockIdx.x;
-    const int tid = threadIdx.x;
-    const T* x = row_at<const T>(a.x, row);
-    const float* st = a.stats + row * kStats;
-    const float m = st[0], ls = st[1], gm = st[2], gls = st[3], Z = st[4];
-    if (!load_list<T, kThreads>(a, row, x, list) || m == neg_inf()) return zero_row<T>(a.g, row);
-    const float w = (a.weights ? a.weights[row] : 1.f) * a.sc.inv;
-    // the teacher's shares
-    float ym = neg_inf(), sum = 0.f;
-    if (!a.rest) {
-        for (int k = 0; k < a.K; ++k)
-            if (list.ok[k]) ym = max_nan(ym, list.y[k]);
-        for (int k = 0; k < a.K; ++k)
-            if (list.ok[k]) sum += expf((list.y[k] - ym) * a.sc.inv);
-    } else {
-        for (int k = 0; k < a.K; ++k)
-            if (list.ok[k]) sum += expf(list.y[k]);
-    }
-    for (int k = tid; k < a.K; k += kThreads)
-        q[k] = !list.ok[k] ? 0.f : a.rest ? expf(list.y[k]) : expf((list.y[k] - ym) * a.sc.inv) / sum;
-    float coef = Z;
-    if (a.rest) {  // Z - sum is q_r: at least kLeastRest, or 0 and what rounding makes of it
-        const float q_r = Z - sum > 0.5f * (float)kLeastRest ? Z - sum : 0.f;
-        coef = Z * expf((gm - m) * a.sc.inv + gls - ls) - q_r;
-    }
-    coef *= w;
-    const float gls2 = gls * kLog2e;
+template <class T, int TEAM>
+__global__ void __launch_bounds__(kThreads) distill_bwd_kernel(const DistillArgs a, int parts) {
+    using Tm = Team<TEAM>;
+    __shared__ ListBuf lists[Tm::kPerCta];
+    const int64_t row = row_of<TEAM>(a.N, parts);
+    if (row < 0) return;
     T* o = row_at<T>(a.g, row);
-    for (int i = tid; i < a.x.M; i += kThreads)
-        o[i] = Elem<T>::put(coef * ex2(fmaf(Elem<T>::get(x[i]) - gm, a.sc.c, -gls2)));
-    __syncthreads();
-    for (int k = tid; k < a.K; k += kThreads)
-        if (list.ok[k] && list.first[k]) {
-            float qs = 0.f;
-            for (int j = k; j < a.K; ++j)
-                if (list.id[j] == list.id[k]) qs += q[j];
-            o[list.id[k]] = Elem<T>::put(w * (Z * expf((list.x[k] - m) * a.sc.inv - ls) - qs));
-        }
+    const Range r = range_of(o, a.x.M, TEAM == 32 ? 0 : blockIdx.x % parts, parts);
+    const T* p = row_at<const T>(a.x, row);
+    ListBuf& list = lists[Tm::id()];
+    const float* st = a.stats + row * kStats;
+    if (!load_list<T, TEAM>(a, row, p, list, r.e0, r.e1) || st[0] == neg_inf()) return zero_range<T, TEAM>(o, r.e0, r.e1);
+    const bool twice = mark_first<TEAM>(list, a.K);
+    if (TEAM == 32 || threadIdx.x < 32) shares(a, list);
+    Tm::sync();
+    RowStats s;
+    s.m = st[0], s.ls = st[1], s.gm = st[2], s.gls = st[3], s.Z = st[4], s.coef = st[5];
+    const float w = (a.weights ? a.weights[row] : 1.f) * a.sc.inv;
+    distill_row_grad<T, TEAM>(a, s, w, o, r.e0, r.e1, FromRow<T>(p, a.x.M, o));
+    Tm::sync();
+    distill_list_grad<T, TEAM>(a, s, w, o, r.e0, r.e1, list, twice);
 }
+
+// 16-byte vectors a CTA should keep when few rows are split
+constexpr int64_t kLeast = kThreads * kUnroll;
 
 template <class T>
 void run_logprobs(const LogprobArgs& a, cudaStream_t s) {
     HookScope h("token_logprobs_backward", s);
-    logprobs_bwd_kernel<T><<<(unsigned)a.N, kThreads, 0, s>>>(a);
+    const Shape sh = shape_of(a.N, a.x.M, true, kLeast * Elem<T>::kVec);
+    const int parts = sh.cluster;
+    if (sh.warp) {
+        if (a.g_entropy) logprobs_bwd_kernel<T, 32, true><<<sh.grid, kThreads, 0, s>>>(a, 1);
+        else logprobs_bwd_kernel<T, 32, false><<<sh.grid, kThreads, 0, s>>>(a, 1);
+    } else {
+        if (a.g_entropy) logprobs_bwd_kernel<T, kThreads, true><<<sh.grid, kThreads, 0, s>>>(a, parts);
+        else logprobs_bwd_kernel<T, kThreads, false><<<sh.grid, kThreads, 0, s>>>(a, parts);
+    }
 }
 template <class T>
 void run_distill(const DistillArgs& a, cudaStream_t s) {
     HookScope h("topk_distillation_backward", s);
-    distill_bwd_kernel<T><<<(unsigned)a.N, kThreads, 0, s>>>(a);
+    const Shape sh = shape_of(a.N, a.x.M, true, kLeast * Elem<T>::kVec);
+    if (sh.warp) distill_bwd_kernel<T, 32><<<sh.grid, kThreads, 0, s>>>(a, 1);
+    else distill_bwd_kernel<T, kThreads><<<sh.grid, kThreads, 0, s>>>(a, sh.cluster);
 }
 
 }  // namespace

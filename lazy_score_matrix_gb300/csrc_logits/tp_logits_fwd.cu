@@ -9,118 +9,222 @@ namespace tp {
 namespace rows {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kUnroll = 4;  // 16-byte vectors in flight per thread
-constexpr int kCap = 1024;  // candidates kept before they are cut back to the best `top`
-
-// Alternatives. Candidates (keys) collect in shared memory; `thr` is the key of the top-th best known so far
-// and candidates at or below it are dropped. When the buffer is full it is sorted and cut to its best `top`.
+// Alternatives. Candidates (keys) collect in shared memory; keys at or below `thr` cannot be among the best
+// `top` and are dropped. When the buffer is full it is cut back to at most kSlack keys more than `top`.
+constexpr int kSlack = 16;
+template <int TEAM>
 struct TopBuf {
+    static constexpr int kCap = TEAM == 32 ? 256 : kMaxCluster * (kMaxList + kSlack);
     unsigned long long key[kCap];
     unsigned long long thr;
     int cnt;
+    uint32_t slot[3];  // reductions of a CTA, in turn: one in use, one read, one cleared
 };
 
-// key[0..n) sorted descending, n a power of two (bitonic network). Ends with a barrier.
-template <int TPB>
-__device__ __forceinline__ void block_sort(unsigned long long* key, int n) {
-    for (int size = 2; size <= n; size <<= 1)
-        for (int stride = size >> 1; stride; stride >>= 1) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < n / 2; i += TPB) {
-                const int a = 2 * i - (i & (stride - 1)), b = a + stride;
-                const unsigned long long x = key[a], y = key[b];
-                const bool down = (a & size) == 0;
-                if ((x < y) == down) key[a] = y, key[b] = x;
-            }
-        }
-    __syncthreads();
-}
+template <int TEAM>
+struct Tops {
+    using Buf = TopBuf<TEAM>;
+    static constexpr int kPer = (Buf::kCap + TEAM - 1) / TEAM;  // keys a thread looks at
+    Buf& b;
+    const int top;
+    int turn = 0;
 
-// The candidates sorted, best first, in key[0..min(cnt, top)); returns that count. Barriers on both sides.
-template <int TPB>
-__device__ __forceinline__ int top_sorted(TopBuf& b, int top) {
-    __syncthreads();
-    const int cnt = min(b.cnt, kCap);
-    int n = 2;
-    while (n < cnt) n <<= 1;
-    for (int i = cnt + threadIdx.x; i < n; i += TPB) b.key[i] = 0;
-    block_sort<TPB>(b.key, n);
-    return min(cnt, top);
-}
-
-// Offer this thread's elements of a chunk: bit i of `mask` stands for column col(i), value val(i).
-template <int TPB, class Col, class Val>
-__device__ __forceinline__ void top_offer(TopBuf& b, int top, uint32_t mask, Col col, Val val) {
-    while (true) {
-        uint32_t left = 0;
-        const unsigned long long thr = b.thr;
-        for (uint32_t m = mask; m; m &= m - 1) {
-            const int i = __ffs(m) - 1;
-            const unsigned long long k = key_of(val(i), col(i));
-            if (k <= thr) continue;
-            const int at = atomicAdd(&b.cnt, 1);
-            if (at < kCap) b.key[at] = k;
-            else left |= 1u << i;
-        }
-        mask = left;
-        if (!__syncthreads_or(mask != 0)) return;
-        const int have = top_sorted<TPB>(b, top);  // the buffer was full: have == top
-        if (threadIdx.x == 0) b.cnt = have, b.thr = b.key[have - 1];
-        __syncthreads();
+    __device__ __forceinline__ Tops(Buf& b_, int top_) : b(b_), top(top_) {}
+    __device__ __forceinline__ void clear() {
+        if (Team<TEAM>::tid() == 0) b.cnt = 0, b.thr = 0, b.slot[0] = b.slot[1] = b.slot[2] = 0;
+        Team<TEAM>::sync();
     }
+    template <class Op, class Warp>
+    __device__ __forceinline__ uint32_t reduce(uint32_t v, Op op, Warp warp) {
+        v = warp(v);
+        if (TEAM == 32) return v;
+        uint32_t* s = &b.slot[turn];
+        if ((threadIdx.x & 31) == 0) op(s, v);
+        __syncthreads();
+        v = *s;
+        turn = turn == 2 ? 0 : turn + 1;  // the slot after it was cleared a barrier ago
+        if (threadIdx.x == 0) b.slot[turn == 2 ? 0 : turn + 1] = 0;
+        return v;
+    }
+    __device__ __forceinline__ uint32_t sum(uint32_t v) {
+        return reduce(v, [](uint32_t* s, uint32_t x) { atomicAdd(s, x); }, [](uint32_t x) { return __reduce_add_sync(~0u, x); });
+    }
+    __device__ __forceinline__ uint32_t max(uint32_t v) {
+        return reduce(v, [](uint32_t* s, uint32_t x) { atomicMax(s, x); }, [](uint32_t x) { return __reduce_max_sync(~0u, x); });
+    }
+
+    // A key that at least k of the team's cnt keys (all above `above`) reach, by bisection, until at most `limit`
+    // do or the bounds are `grain` apart. `key` are the thread's own of them (0: none).
+    __device__ __forceinline__ unsigned long long bound(const unsigned long long (&key)[kPer], int cnt, int k, int limit,
+                                                        unsigned long long above, unsigned long long grain) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int r = 0; r < kPer; ++r) m = ::max(m, (uint32_t)(key[r] >> 32));
+        unsigned long long lo = above + 1, hi = ((unsigned long long)max(m) + 1) << 32;
+        int n = cnt;
+        while (n > limit && hi - lo > grain) {
+            const unsigned long long mid = lo + (hi - lo) / 2;
+            uint32_t c = 0;
+#pragma unroll
+            for (int r = 0; r < kPer; ++r) c += key[r] >= mid;
+            c = sum(c);
+            if ((int)c >= k) lo = mid, n = (int)c;
+            else hi = mid;
+        }
+        return lo;
+    }
+    // Cuts the buffer back to at most top + kSlack keys, the best `top` among them. Barriers on both sides.
+    __device__ __forceinline__ void cut() {
+        Team<TEAM>::sync();
+        const int t = Team<TEAM>::tid(), cnt = min(b.cnt, Buf::kCap);
+        if (cnt <= top + kSlack) return;
+        unsigned long long key[kPer];
+#pragma unroll
+        for (int r = 0; r < kPer; ++r) key[r] = t + r * TEAM < cnt ? b.key[t + r * TEAM] : 0;
+        const unsigned long long lo = bound(key, cnt, top, top + kSlack, b.thr, 1);
+        Team<TEAM>::sync();
+        if (t == 0) b.cnt = 0, b.thr = lo - 1;
+        Team<TEAM>::sync();
+#pragma unroll
+        for (int r = 0; r < kPer; ++r)
+            if (key[r] >= lo) b.key[atomicAdd(&b.cnt, 1)] = key[r];
+        Team<TEAM>::sync();
+    }
+    // A first threshold, from every thread's best value so far: `top` threads that reach it are as many columns.
+    // `grain`: the step of the scores' type in a key (fp16 and bf16 leave the low bits of an fp32 value alone).
+    __device__ __forceinline__ void start(float best, unsigned long long grain) {
+        unsigned long long key[kPer];
+#pragma unroll
+        for (int r = 0; r < kPer; ++r) key[r] = 0;
+        if (best > neg_inf()) key[0] = (unsigned long long)ord_of(best) << 32;
+        const int have = (int)sum(key[0] != 0);
+        if (have < top) return;
+        const unsigned long long lo = bound(key, have, top, top + top / 8, 0, grain);
+        if (Team<TEAM>::tid() == 0) b.thr = lo - 1;
+        Team<TEAM>::sync();
+    }
+    // The value that a column from `col` on has to reach. A key at the threshold's value but of a later column
+    // is below the threshold, so the bar is then one step higher.
+    __device__ __forceinline__ float bar(int64_t col) const {
+        const unsigned long long thr = b.thr;
+        if (thr == 0) return __uint_as_float(0xff7fffffu);  // anything above -inf
+        const uint32_t o = ::max((uint32_t)(thr >> 32), 0x00800000u);  // a bound may lie below every finite value
+        return of_ord((int64_t)(uint32_t)~(uint32_t)thr < col ? o + 1 : o);
+    }
+    // Offer this thread's elements of a chunk: bit i of `mask` stands for column col(i), value val(i).
+    template <class Col, class Val>
+    __device__ __forceinline__ void offer(uint32_t mask, Col col, Val val) {
+        while (true) {
+            uint32_t left = 0;
+            const unsigned long long thr = b.thr;
+            for (uint32_t m = mask; m; m &= m - 1) {
+                const int i = __ffs(m) - 1;
+                const unsigned long long k = key_of(val(i), col(i));
+                if (k <= thr) continue;
+                const int at = atomicAdd(&b.cnt, 1);
+                if (at < Buf::kCap) b.key[at] = k;
+                else left |= 1u << i;
+            }
+            mask = left;
+            if (!Team<TEAM>::any(mask != 0)) return;
+            cut();
+        }
+    }
+};
+
+// What a row that does not count gives.
+__device__ __forceinline__ void leave_out(const LogprobArgs& a, int64_t row, int t, int team) {
+    if (t == 0) {
+        a.logprobs[row] = 0.f, a.entropy[row] = 0.f;
+        if (a.stats)
+            for (int i = 0; i < kStats; ++i) a.stats[row * kStats + i] = 0.f;
+    }
+    for (int i = t; i < a.top; i += team) a.top_logprobs[row * a.top + i] = neg_inf(), a.top_ids[row * a.top + i] = -1;
 }
 
-template <class T, bool TOP>
+struct Gather {  // the candidates of a cluster's other CTAs
+    unsigned long long key[kMaxCluster][kMaxList + kSlack];
+    int n[kMaxCluster];
+};
+
+template <class T, int TEAM, bool TOP>
 __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a) {
     constexpr int V = Elem<T>::kVec;
+    using Tm = Team<TEAM>;
     __shared__ ReduceBuf red;
-    __shared__ TopBuf tops;
-    const int64_t row = blockIdx.x;
-    const int tid = threadIdx.x;
+    __shared__ ClusterBuf parts;
+    __shared__ TopBuf<TEAM> tops[TOP ? Tm::kPerCta : 1];
+    __shared__ Gather others[1];
+    const int rank = TEAM == 32 ? 0 : cluster_rank(), size = TEAM == 32 ? 1 : cluster_size();
+    const int64_t row = TEAM == 32 ? (int64_t)blockIdx.x * Tm::kPerCta + Tm::id() : blockIdx.x / size;
+    if (row >= a.N) return;
+    const int t = Tm::tid();
     const int64_t tok = a.tokens ? a.tokens[row] : 0;
-    if (tok < 0 || tok >= a.x.M) {  // left out: nothing is read
-        if (tid == 0) {
-            a.logprobs[row] = 0.f, a.entropy[row] = 0.f;
-            if (a.stats)
-                for (int i = 0; i < kStats; ++i) a.stats[row * kStats + i] = 0.f;
-        }
-        for (int i = tid; i < a.top; i += kThreads) a.top_logprobs[row * a.top + i] = neg_inf(), a.top_ids[row * a.top + i] = -1;
+    if (tok < 0 || tok >= a.x.M) {
+        if (rank == 0) leave_out(a, row, t, TEAM);
         return;
     }
+    if (size > 1) cluster_arrive();
     const RowVecs<T> x(row_at<const T>(a.x, row), a.x.M);
-    if (TOP) {
-        if (tid == 0) tops.cnt = 0, tops.thr = 0;
-        __syncthreads();
-    }
+    const Slice sl = slice_of(x.n, rank, size);
+    Tops<TEAM> best(tops[TOP ? Tm::id() : 0], a.top);
+    if (TOP) best.clear();
     State st;
-    for (int base = 0; base < x.n; base += kThreads * kUnroll) {
+    for (int base = sl.begin; base < sl.end; base += TEAM * kUnroll) {
         float f[kUnroll * V];
-        if (x.inside(base, base + kThreads * kUnroll)) {
+        if (base + TEAM * kUnroll <= sl.end && x.inside(base, base + TEAM * kUnroll)) {
             uint4 r[kUnroll];
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) r[u] = x.raw(base + u * kThreads + tid);
+            for (int u = 0; u < kUnroll; ++u) r[u] = x.raw(base + u * TEAM + t);
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) Elem<T>::unpack(r[u], f + u * V);
         } else {
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) x.edge(base + u * kThreads + tid, f + u * V);
+            for (int u = 0; u < kUnroll; ++u) {
+                const int j = base + u * TEAM + t;
+                x.edge(j < sl.end ? j : x.n, f + u * V);
+            }
         }
         add_scores(st, f, a.sc.c);
         if (TOP) {
-            const float bar = tops.thr ? of_ord((uint32_t)(tops.thr >> 32)) : neg_inf();
+            if (base == sl.begin) best.start(st.m, sizeof(T) == 2 ? 1ull << 44 : 1ull << 32);
+            const float bar = best.bar(x.first(base));
             uint32_t mask = 0;
 #pragma unroll
-            for (int i = 0; i < kUnroll * V; ++i) mask |= (f[i] > neg_inf() && f[i] >= bar) ? 1u << i : 0u;
-            const auto col = [&](int i) { return (int)(x.first(base + (i / V) * kThreads + tid) + i % V); };
-            top_offer<kThreads>(tops, a.top, mask, col, [&](int i) { return Elem<T>::get(x.p[col(i)]); });
+            for (int i = 0; i < kUnroll * V; ++i) mask |= f[i] >= bar ? 1u << i : 0u;
+            const auto col = [&](int i) { return (int)(x.first(base + (i / V) * TEAM + t) + i % V); };
+            best.offer(mask, col, [&](int i) { return Elem<T>::get(x.p[col(i)]); });
         }
     }
-    st = block_state<kThreads>(st, a.sc.c, red);
+    st = team_state<TEAM>(st, a.sc.c, red);
+    if (size > 1) {
+        if (TOP) best.cut();
+        cluster_wait();  // every CTA of the cluster runs
+        cluster_share(st, parts, rank, size);
+        if (TOP) {
+            Gather* g = of_rank(&others[0], 0);
+            const int n = min(best.b.cnt, a.top + kSlack);
+            for (int i = t; i < n; i += TEAM) g->key[rank][i] = best.b.key[i];
+            if (t == 0) g->n[rank] = n;
+        }
+        cluster_arrive();
+        cluster_wait();
+        if (rank != 0) return;
+        st = cluster_merge(parts, size, a.sc.c);
+        if (TOP) {
+            int at = 0;
+            for (int r = 0; r < size; ++r) {
+                const int n = others[0].n[r];
+                for (int i = t; i < n; i += TEAM) best.b.key[at + i] = others[0].key[r][i];
+                at += n;
+            }
+            if (t == 0) best.b.cnt = at, best.b.thr = 0;
+        }
+    }
     const bool some = st.m != neg_inf();
     const float z = st.s + (st.lo + a.sc.delta * st.h);
     const float ls = some ? logf(z) : 0.f;
-    if (tid == 0) {
+    if (t == 0) {
         const float H = some ? ls - st.h / z * a.sc.inv : 0.f;
         a.entropy[row] = H;
         if (a.logprobs) a.logprobs[row] = some ? (Elem<T>::get(x.p[tok]) - st.m) * a.sc.inv - ls : neg_inf();
@@ -131,168 +235,148 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
         }
     }
     if (TOP) {
-        const int have = top_sorted<kThreads>(tops, a.top);
-        for (int i = tid; i < a.top; i += kThreads) {
-            const unsigned long long k = tops.key[i < have ? i : 0];
-            a.top_logprobs[row * a.top + i] = i < have ? (of_ord((uint32_t)(k >> 32)) - st.m) * a.sc.inv - ls : neg_inf();
-            a.top_ids[row * a.top + i] = i < have ? (int64_t)(~(uint32_t)k) : -1;
+        best.cut();
+        const int n = min(best.b.cnt, a.top + kSlack);
+        for (int i = t; i < n; i += TEAM) {  // the keys differ: a key's place is the number of larger ones
+            const unsigned long long k = best.b.key[i];
+            int place = 0;
+            for (int j = 0; j < n; ++j) place += best.b.key[j] > k;
+            if (place < a.top) {
+                a.top_logprobs[row * a.top + place] = (of_ord((uint32_t)(k >> 32)) - st.m) * a.sc.inv - ls;
+                a.top_ids[row * a.top + place] = (int64_t)(~(uint32_t)k);
+            }
         }
+        for (int i = n + t; i < a.top; i += TEAM) a.top_logprobs[row * a.top + i] = neg_inf(), a.top_ids[row * a.top + i] = -1;
     }
 }
 
-constexpr int kMarkCols = 1 << 16;  // unlisted columns are told by a bit map of this many columns at a time
+// Unlisted columns are told by a bit map of this many columns of the row at a time.
+template <int TEAM>
+struct Marks {
+    static constexpr int kCols = TEAM == 32 ? 1 << 12 : 1 << 16;
+    uint32_t bits[kCols / 32];
+    // bit i of the map becomes: element e0 + i is listed. Barriers on both sides.
+    __device__ __forceinline__ void set(const ListBuf& l, int K, int64_t e0) {
+        Team<TEAM>::sync();
+        for (int i = Team<TEAM>::tid(); i < kCols / 32; i += TEAM) bits[i] = 0;
+        Team<TEAM>::sync();
+        for (int k = Team<TEAM>::tid(); k < K; k += TEAM) {
+            const int64_t at = l.ok(k) ? l.id[k] - e0 : -1;
+            if (at >= 0 && at < kCols) atomicOr(&bits[at >> 5], 1u << (at & 31));
+        }
+        Team<TEAM>::sync();
+    }
+};
 
-// The list's part of a row, by one warp: teacher's shares q, the loss, and the row's statistics. `st` is the
-// state of all columns (plain) or of the unlisted ones (rest). In fp64: what is left of a loss near zero is
-// the difference of logarithms that agree to several digits.
-__device__ __forceinline__ void distill_row(const DistillArgs& a, int64_t row, const State& st, const ListBuf& l) {
-    const int lane = threadIdx.x & 31;
-    const double inv = a.sc.inv64;
-    const double zs = exact_sum(st, a.sc);
-    float m = st.m;       // maximum over all columns
-    double z = zs;        // sum over all columns, relative to m
-    double q[4], lq[4];
-    if (a.rest) {
-        float lm = neg_inf();
-        for (int j = 0; j < 4; ++j) {
-            const int k = lane + 32 * j;
-            if (k < a.K && l.ok[k]) lm = max_nan(lm, l.x[k]);
-        }
-        m = max_nan(st.m, warp_max(lm));
-        double sum = 0;
-        for (int j = 0; j < 4; ++j) {
-            const int k = lane + 32 * j;
-            if (k < a.K && l.ok[k] && l.first[k] && l.x[k] > neg_inf()) sum += exp_table(((double)l.x[k] - m) * inv);
-        }
-        z = warp_sum64(sum);
-        if (st.m > neg_inf()) z += zs * exp_table(((double)st.m - m) * inv);
-        if (m != m) z = m;  // NaN
-        for (int j = 0; j < 4; ++j) {
-            const int k = lane + 32 * j;
-            const bool ok = k < a.K && l.ok[k];
-            lq[j] = ok ? l.y[k] : 0.0;
-            q[j] = ok ? exp_table(lq[j]) : 0.0;
-        }
-    } else {
-        float ym = neg_inf();
-        for (int j = 0; j < 4; ++j) {
-            const int k = lane + 32 * j;
-            if (k < a.K && l.ok[k]) ym = max_nan(ym, l.y[k]);
-        }
-        ym = warp_max(ym);
-        double sum = 0;
-        for (int j = 0; j < 4; ++j) {
-            const int k = lane + 32 * j;
-            const bool ok = k < a.K && l.ok[k];
-            lq[j] = ok ? ((double)l.y[k] - ym) * inv : 0.0;
-            q[j] = ok ? exp_table(lq[j]) : 0.0;
-            sum += q[j];
-        }
-        sum = warp_sum64(sum);
-        const double ln = ln64(sum), r = 1.0 / sum;
-        for (int j = 0; j < 4; ++j) q[j] *= r, lq[j] -= ln;
-    }
-    const double m0 = m == neg_inf() ? 0.0 : (double)m, ls = m == neg_inf() ? 0.0 : ln64(z);
-    double loss = 0, Z = 0;
-    for (int j = 0; j < 4; ++j) {
-        const int k = lane + 32 * j;
-        if (q[j] > 0) loss += q[j] * (lq[j] - (((double)l.x[k] - m0) * inv - ls));
-        Z += q[j];
-    }
-    loss = warp_sum64(loss), Z = warp_sum64(Z);
-    float gm = m, gls = (float)ls;
-    if (a.rest && st.m != neg_inf()) {
-        const double q_r = 1.0 - Z >= kLeastRest ? 1.0 - Z : 0.0, lr = ln64(zs), lp = ((double)st.m - m0) * inv + lr - ls;
-        if (q_r > 0) loss += q_r * (ln64(q_r) - lp);
-        Z += q_r;
-        gm = st.m, gls = (float)lr;
-    }
-    if (lane == 0) {
-        a.loss[row] = (float)loss;
-        if (a.stats) {
-            float* o = a.stats + row * kStats;
-            o[0] = m, o[1] = (float)ls, o[2] = gm, o[3] = gls, o[4] = (float)Z;
-            o[5] = o[6] = o[7] = 0.f;
-        }
-    }
-}
-
-template <class T, bool REST>
+template <class T, int TEAM, bool REST>
 __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillArgs a) {
     constexpr int V = Elem<T>::kVec;
+    using Tm = Team<TEAM>;
     __shared__ ReduceBuf red;
-    __shared__ ListBuf list;
-    __shared__ uint32_t marks[REST ? kMarkCols / 32 + 2 : 1];
-    const int64_t row = blockIdx.x;
-    const int tid = threadIdx.x;
+    __shared__ ClusterBuf parts;
+    __shared__ ListBuf lists[Tm::kPerCta];
+    __shared__ Marks<TEAM> marks[REST ? Tm::kPerCta : 1];
+    const int rank = TEAM == 32 ? 0 : cluster_rank(), size = TEAM == 32 ? 1 : cluster_size();
+    const int64_t row = TEAM == 32 ? (int64_t)blockIdx.x * Tm::kPerCta + Tm::id() : blockIdx.x / size;
+    if (row >= a.N) return;
+    const int t = Tm::tid();
     const T* p = row_at<const T>(a.x, row);
-    if (!load_list<T, kThreads>(a, row, p, list)) {
-        if (tid == 0) {
+    ListBuf& list = lists[Tm::id()];
+    if (!load_list<T, TEAM>(a, row, p, list, 0, a.x.M)) {
+        if (rank == 0 && t == 0) {
             a.loss[row] = 0.f;
             if (a.stats)
                 for (int i = 0; i < kStats; ++i) a.stats[row * kStats + i] = 0.f;
         }
         return;
     }
+    if (size > 1) cluster_arrive();
     const RowVecs<T> x(p, a.x.M);
-    constexpr int kMarkVecs = kMarkCols / V;
+    const Slice sl = slice_of(x.n, rank, size);
+    constexpr int kMarkVecs = Marks<TEAM>::kCols / V;
+    if (REST) mark_first<TEAM>(list, a.K);
     State st;
-    for (int part = 0; part < x.n; part += kMarkVecs) {
-        if (REST) {  // bit i of the map is element first(part) + i
-            __syncthreads();
-            for (int i = tid; i < kMarkCols / 32 + 2; i += kThreads) marks[i] = 0;
-            __syncthreads();
-            for (int k = tid; k < a.K; k += kThreads) {
-                const int64_t at = list.ok[k] ? list.id[k] - x.first(part) : -1;
-                if (at >= 0 && at < kMarkCols) atomicOr(&marks[at >> 5], 1u << (at & 31));
-            }
-            __syncthreads();
-        }
-        const int end = min(x.n, part + kMarkVecs);
-        for (int base = part; base < end; base += kThreads * kUnroll) {
+    for (int part = sl.begin; part < sl.end; part += kMarkVecs) {
+        if (REST) marks[Tm::id()].set(list, a.K, x.first(part));
+        const int end = min(sl.end, part + kMarkVecs);
+        for (int base = part; base < end; base += TEAM * kUnroll) {
             float f[kUnroll * V];
-            if (base + kThreads * kUnroll <= end && x.inside(base, base + kThreads * kUnroll)) {
+            if (base + TEAM * kUnroll <= end && x.inside(base, base + TEAM * kUnroll)) {
                 uint4 r[kUnroll];
 #pragma unroll
-                for (int u = 0; u < kUnroll; ++u) r[u] = x.raw(base + u * kThreads + tid);
+                for (int u = 0; u < kUnroll; ++u) r[u] = x.raw(base + u * TEAM + t);
 #pragma unroll
                 for (int u = 0; u < kUnroll; ++u) Elem<T>::unpack(r[u], f + u * V);
             } else {
 #pragma unroll
                 for (int u = 0; u < kUnroll; ++u) {
-                    const int j = base + u * kThreads + tid;
+                    const int j = base + u * TEAM + t;
                     x.edge(j < end ? j : x.n, f + u * V);
                 }
             }
             if (REST) {
 #pragma unroll
                 for (int u = 0; u < kUnroll; ++u) {
-                    const int bit = (base - part + u * kThreads + tid) * V;
-                    if (bit >= kMarkCols) continue;
-                    const uint32_t w = marks[bit >> 5] >> (bit & 31);
+                    const int bit = (base - part + u * TEAM + t) * V;
+                    const uint32_t w = marks[Tm::id()].bits[(bit >> 5) & (Marks<TEAM>::kCols / 32 - 1)] >> (bit & 31);
+                    if (w & ((1u << V) - 1)) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        if (w & (1u << i)) f[u * V + i] = neg_inf();
+                        for (int i = 0; i < V; ++i)
+                            if (w & (1u << i)) f[u * V + i] = neg_inf();
+                    }
                 }
             }
             add_scores(st, f, a.sc.c);
         }
     }
-    st = block_state<kThreads>(st, a.sc.c, red);
-    if (tid < 32) distill_row(a, row, st, list);
+    st = team_state<TEAM>(st, a.sc.c, red);
+    if (size > 1) {
+        cluster_wait();  // every CTA of the cluster runs
+        cluster_share(st, parts, rank, size);
+        cluster_arrive();
+        cluster_wait();
+        if (rank != 0) return;
+        st = cluster_merge(parts, size, a.sc.c);
+    }
+    if (TEAM == 32 || threadIdx.x < 32) {
+        const RowStats s = distill_row(a, st, list);
+        if (t == 0) {
+            a.loss[row] = s.loss;
+            if (a.stats) {
+                float* o = a.stats + row * kStats;
+                o[0] = s.m, o[1] = s.ls, o[2] = s.gm, o[3] = s.gls, o[4] = s.Z, o[5] = s.coef;
+                o[6] = o[7] = 0.f;
+            }
+        }
+    }
 }
+
+template <class T>
+constexpr int64_t kChunk = kThreads * kUnroll * Elem<T>::kVec;
 
 template <class T>
 void run_logprobs(const LogprobArgs& a, cudaStream_t s) {
     HookScope h("token_logprobs", s);
-    if (a.top) logprobs_kernel<T, true><<<(unsigned)a.N, kThreads, 0, s>>>(a);
-    else logprobs_kernel<T, false><<<(unsigned)a.N, kThreads, 0, s>>>(a);
+    const Shape sh = shape_of(a.N, a.x.M, a.top <= 32, kChunk<T>);
+    if (sh.warp) {
+        if (a.top) launch(logprobs_kernel<T, 32, true>, sh, s, a);
+        else launch(logprobs_kernel<T, 32, false>, sh, s, a);
+    } else {
+        if (a.top) launch(logprobs_kernel<T, kThreads, true>, sh, s, a);
+        else launch(logprobs_kernel<T, kThreads, false>, sh, s, a);
+    }
 }
 template <class T>
 void run_distill(const DistillArgs& a, cudaStream_t s) {
     HookScope h("topk_distillation", s);
-    if (a.rest) distill_kernel<T, true><<<(unsigned)a.N, kThreads, 0, s>>>(a);
-    else distill_kernel<T, false><<<(unsigned)a.N, kThreads, 0, s>>>(a);
+    const Shape sh = shape_of(a.N, a.x.M, true, kChunk<T>);
+    if (sh.warp) {
+        if (a.rest) launch(distill_kernel<T, 32, true>, sh, s, a);
+        else launch(distill_kernel<T, 32, false>, sh, s, a);
+    } else {
+        if (a.rest) launch(distill_kernel<T, kThreads, true>, sh, s, a);
+        else launch(distill_kernel<T, kThreads, false>, sh, s, a);
+    }
 }
 
 }  // namespace

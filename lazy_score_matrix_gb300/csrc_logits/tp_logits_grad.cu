@@ -1,0 +1,230 @@
+// topk_distillation_grad: loss and gradient of a row from one reading of it. The row's scores stay on chip between
+// the two: each CTA of a cluster copies a slice of the row into its shared memory, the softmax states meet
+// through distributed shared memory, and the gradient is written from the slices.
+//
+// Traffic is one read of the scores and one write of the gradient, which is all the operator has to move; the
+// forward and backward kernels in a row read the scores twice. What bounds it is memory, as long as enough
+// slices are resident to cover the time between a slice's last load and its first store (reduction, cluster
+// barrier, the list's arithmetic).
+#include <cuda_runtime.h>
+
+#include <atomic>
+
+#include "tp_launch.h"
+#include "tp_logits.cuh"
+#include "tp_logits_out.cuh"
+
+namespace tp {
+namespace rows {
+namespace {
+
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// wait until at most `left` of the thread's groups of copies are under way
+__device__ __forceinline__ void copies_wait(int left) {
+    if (left >= 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else if (left == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (left == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// The scores of a slice in shared memory (vectors of the scores' alignment), fetched for vectors of the
+// gradient's alignment.
+template <class T>
+struct FromSlice {
+    static constexpr int V = Elem<T>::kVec;
+    const uint4* buf;
+    int64_t e0;  // element at buf[0]
+    int n;       // vectors
+    __device__ __forceinline__ bool get(int64_t e, uint4& v) const {
+        const int at = (int)(e - e0), j = at / V, shift = (at % V) * (int)sizeof(T);
+        if (at < 0 || j >= n || (shift && j + 1 >= n)) return false;
+        v = shift ? window(buf[j], buf[j + 1], shift) : buf[j];
+        return true;
+    }
+    __device__ __forceinline__ float one(int64_t e) const { return Elem<T>::get(reinterpret_cast<const T*>(buf)[e - e0]); }
+};
+
+template <class T, int TEAM, bool REST>
+__global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillArgs a, int room) {
+    constexpr int V = Elem<T>::kVec;
+    using Tm = Team<TEAM>;
+    extern __shared__ uint4 dyn[];  // per team: room vectors, then (rest) one bit per element of them
+    __shared__ ReduceBuf red;
+    __shared__ ClusterBuf parts;
+    __shared__ ListBuf lists[Tm::kPerCta];
+    __shared__ RowStats shared_stats;
+    const int words = REST ? room * V / 32 : 0;  // room is a multiple of 32
+    uint4* buf = dyn + (size_t)Tm::id() * (room + words / 4);
+    uint32_t* marks = reinterpret_cast<uint32_t*>(buf + room);
+    const int rank = TEAM == 32 ? 0 : cluster_rank(), size = TEAM == 32 ? 1 : cluster_size();
+    const int64_t row = TEAM == 32 ? (int64_t)blockIdx.x * Tm::kPerCta + Tm::id() : blockIdx.x / size;
+    if (row >= a.N) return;
+    const int t = Tm::tid();
+    const T* p = row_at<const T>(a.x, row);
+    T* o = row_at<T>(a.g, row);
+    ListBuf& list = lists[Tm::id()];
+    const RowVecs<T> x(p, a.x.M);
+    const Slice sl = slice_of(x.n, rank, size);
+    const int n = sl.end - sl.begin;
+    // the slice's elements, and the gradient's vectors that hold them (the first and the last may be shared with
+    // a neighbouring slice and are then written element by element)
+    const int64_t s0 = x.first(sl.begin), e0 = max(s0, (int64_t)0), e1 = min(x.first(sl.end), (int64_t)a.x.M);
+    if (!load_list<T, TEAM>(a, row, p, list, 0, a.x.M)) {
+        if (rank == 0 && t == 0) {
+            a.loss[row] = 0.f;
+            for (int i = 0; i < kStats; ++i) a.stats[row * kStats + i] = 0.f;
+        }
+        return zero_range<T, TEAM>(o, e0, e1);
+    }
+    if (size > 1) cluster_arrive();
+    // every thread copies the vectors that it will reduce: no barrier stands between the two
+    for (int i = t; i < n; i += TEAM * kUnroll) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int j = i + u * TEAM;
+            if (j >= n) break;
+            if (x.inside(sl.begin + j, sl.begin + j + 1)) {
+                copy_async(buf + j, x.at(sl.begin + j));
+            } else {
+                float f[V];
+                x.edge(sl.begin + j, f);
+                buf[j] = Elem<T>::pack(f);
+            }
+        }
+        copies_end();
+    }
+    const bool twice = mark_first<TEAM>(list, a.K);
+    if (REST) {
+        for (int i = t; i < words; i += TEAM) marks[i] = 0;
+        Tm::sync();
+        for (int k = t; k < a.K; k += TEAM)
+            if (list.ok(k) && list.id[k] >= e0 && list.id[k] < e1) {
+                const int at = (int)(list.id[k] - s0);
+                atomicOr(&marks[at >> 5], 1u << (at & 31));
+            }
+        Tm::sync();
+    }
+    State st;
+    int left = (n - t + TEAM * kUnroll - 1) / (TEAM * kUnroll);  // groups of this thread
+    for (int i = t; i < n; i += TEAM * kUnroll) {
+        copies_wait(--left);
+        float f[kUnroll * V];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int j = i + u * TEAM;
+            if (j < n) {
+                Elem<T>::unpack(buf[j], f + u * V);
+                if (REST) {
+                    const uint32_t w = marks[j * V >> 5] >> (j * V & 31);
+                    if (w & ((1u << V) - 1)) {
+#pragma unroll
+                        for (int k = 0; k < V; ++k)
+                            if (w & (1u << k)) f[u * V + k] = neg_inf();
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < V; ++k) f[u * V + k] = neg_inf();
+            }
+        }
+        add_scores(st, f, a.sc.c);
+    }
+    st = team_state<TEAM>(st, a.sc.c, red);
+    if (size > 1) {
+        cluster_wait();  // every CTA of the cluster runs
+        cluster_share(st, parts, rank, size);
+        cluster_arrive();
+        cluster_wait();
+        st = cluster_merge(parts, size, a.sc.c);
+    }
+    RowStats s;
+    if (TEAM == 32 || threadIdx.x < 32) s = distill_row(a, st, list);
+    if (rank == 0 && t == 0) {
+        a.loss[row] = s.loss;
+        float* q = a.stats + row * kStats;
+        q[0] = s.m, q[1] = s.ls, q[2] = s.gm, q[3] = s.gls, q[4] = s.Z, q[5] = s.coef;
+        q[6] = q[7] = 0.f;
+    }
+    if (TEAM != 32) {
+        if (t == 0) shared_stats = s;
+        __syncthreads();
+        s = shared_stats;
+    } else {
+        __syncwarp();
+    }
+    const float w = (a.weights ? a.weights[row] : 1.f) * a.sc.inv;
+    const FromSlice<T> from{buf, s0, n};
+    if (s.m == neg_inf()) {  // a row of -inf alone
+        zero_range<T, TEAM>(o, e0, e1);
+        return;
+    }
+    distill_row_grad<T, TEAM>(a, s, w, o, e0, e1, from);
+    Tm::sync();
+    distill_list_grad<T, TEAM>(a, s, w, o, e0, e1, list, twice);
+}
+
+constexpr size_t kSmemMost = 200 * 1024;     // a CTA's slice at most
+constexpr size_t kSmemThree = 68 * 1024;     // three CTAs an SM
+constexpr int64_t kWarpBytes = 4096;         // rows up to this long: one warp a row
+
+// Shared memory for slices of n vectors; room receives the vectors per team.
+inline size_t smem_of(int64_t n, int teams, int V, bool rest, int& room) {
+    const int64_t r = (n + 31) / 32 * 32;
+    room = (int)r;
+    return (size_t)teams * (size_t)(r * 16 + (rest ? r * V / 8 : 0));
+}
+
+template <class T, int TEAM, bool REST>
+void go(const DistillArgs& a, const Shape& sh, int room, cudaStream_t s) {
+    auto kernel = distill_grad_kernel<T, TEAM, REST>;
+    static std::atomic<uint64_t> ready{0};  // devices whose limit is raised, bit by bit
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMost) != cudaSuccess) return;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
+    HookScope h("topk_distillation_grad", s);
+    launch(kernel, sh, s, a, room);
+}
+
+template <class T>
+bool run(const DistillArgs& a, cudaStream_t s) {
+    constexpr int V = Elem<T>::kVec;
+    const int64_t n = ((int64_t)a.x.M + 2 * V - 2) / V + 1;  // vectors of a row at any alignment, at most
+    Shape sh;
+    int room = 0;
+    sh.warp = n * 16 <= kWarpBytes && a.N >= kWarpRows;
+    sh.cluster = 1;
+    if (sh.warp) {
+        sh.smem = smem_of(n, 8, V, a.rest, room);
+        sh.grid = (unsigned)((a.N + 7) / 8);
+        if (a.rest) go<T, 32, true>(a, sh, room, s);
+        else go<T, 32, false>(a, sh, room, s);
+        return true;
+    }
+    const auto smem = [&](int c) { return smem_of((n + c - 1) / c, 1, V, a.rest, room); };
+    while (sh.cluster < kMaxCluster && smem(sh.cluster) > kSmemThree) ++sh.cluster;
+    while (sh.cluster < kMaxCluster && a.N * sh.cluster < kFewRows && n >= (int64_t)(sh.cluster + 1) * kThreads) ++sh.cluster;
+    sh.smem = smem(sh.cluster);
+    if (sh.smem > kSmemMost) return false;
+    sh.grid = (unsigned)(a.N * sh.cluster);
+    if (a.rest) go<T, kThreads, true>(a, sh, room, s);
+    else go<T, kThreads, false>(a, sh, room, s);
+    return true;
+}
+
+}  // namespace
+
+bool launch_distill_grad(tp_rows_dtype t, const DistillArgs& a, cudaStream_t s) {
+    if (t == TP_ROWS_F32) return run<float>(a, s);
+    if (t == TP_ROWS_F16) return run<__half>(a, s);
+    return run<__nv_bfloat16>(a, s);
+}
+
+}  // namespace rows
+}  // namespace tp

@@ -326,17 +326,23 @@ def test_offsets_beyond_32_bits():
     big[-3:] = x.to(DEV)
     tok = torch.full((n,), -1, device=DEV)
     tok[-3:] = torch.tensor([5, 6, m - 1], device=DEV)
-    small, want = tp.token_logprobs(big[-3:].clone(), tok[-3:], top=5), tp.token_logprobs(big, tok, top=5)
-    for f in ("logprobs", "entropy", "top_logprobs", "top_ids"):
-        assert torch.equal(getattr(small, f), getattr(want, f)[-3:]), f
+    r = tp.token_logprobs(big, tok, top=5)
     ids, values = teacher_list(x, 7, 1.0, True, 2)
     ids_all = torch.full((n, 7), -1, device=DEV)
     ids_all[-3:] = ids.to(DEV)
     values_all = torch.zeros(n, 7, device=DEV)
     values_all[-3:] = values.to(DEV)
-    loss3, grad3 = tp.topk_distillation_grad(big[-3:].clone(), ids_all[-3:], values_all[-3:], rest=True)
     loss, grad = tp.topk_distillation_grad(big, ids_all, values_all, rest=True, out=big)
-    assert grad is big and torch.equal(loss[-3:], loss3) and torch.equal(grad[-3:], grad3)
+    assert grad is big
+    # against 64 bits, not against a call on these rows alone: that one splits a row over more threads and may
+    # round its sums another way
+    for i, t in enumerate([5, 6, m - 1]):
+        w, e = ref.logprobs(x[i].double(), t, 1.0, 5), ref.distill(x[i].double(), ids[i].tolist(), values[i].tolist(), 1.0, True)
+        ref.close(r.logprobs[n - 3 + i], w["lp"], w["lp_tol"])
+        ref.close(r.entropy[n - 3 + i], w["h"], w["h_tol"])
+        assert r.top_ids[n - 3 + i].tolist() == w["top_ids"]
+        ref.close(loss[n - 3 + i], e["loss"], e["loss_tol"])
+        ref.close(grad[n - 3 + i], e["grad"], e["grad_tol"], torch.bfloat16)
     assert (loss[:-3] == 0).all() and int(torch.count_nonzero(grad[-200:-3])) == 0
 
 
