@@ -36,7 +36,7 @@ typedef enum { TP_ROWS_F32 = 0, TP_ROWS_F16 = 1, TP_ROWS_BF16 = 2 } tp_rows_dtyp
 /* N rows of M scores. Row i starts at element (i / group) * group_stride + (i % group) * row_stride of
  * data; the M scores of a row are adjacent. A plain matrix has group = N (group_stride is then not read);
  * a shifted batch such as logits[:, :-1] of [B, S, M] has group = S - 1, row_stride = M,
- * group_stride = S * M. 1 <= M, N < 2^31; N is a multiple of group; strides are >= 0 elements. Rows that
+ * group_stride = S * M. 1 <= N < 2^31, 1 <= M <= 2^30; N is a multiple of group; strides are >= 0 elements. Rows that
  * are written must not overlap one another. */
 typedef struct {
     tp_rows_dtype dtype;

@@ -93,6 +93,7 @@ LAUNCH_HOOK = ctypes.CFUNCTYPE(None, ctypes.c_char_p, ctypes.c_int, ctypes.c_voi
 
 _lock = threading.Lock()
 _lib = None
+_logits_lib = None
 
 
 class TPError(RuntimeError):
@@ -125,6 +126,22 @@ def load(path: str | None = None):
         if path is None:
             _lib = lib
         return lib
+
+
+def load_logits():
+    """The entries of include/tp_logits.h, called with the interpreter lock held: a call only validates and enqueues
+    (a few microseconds), and handing the lock over around it costs more than that inside an autograd backward,
+    which runs on a thread of its own."""
+    global _logits_lib
+    if _logits_lib is None:
+        load()
+        lib = ctypes.PyDLL(LIB_PATH)
+        for name, (args, res) in LOGITS_SIGNATURES.items():
+            f = getattr(lib, name)
+            f.argtypes = args
+            f.restype = res
+        _logits_lib = lib
+    return _logits_lib
 
 
 def status_text(status: int) -> str:

@@ -14,14 +14,15 @@
 
 #include "tp_device.cuh"
 #include "tp_logits_args.h"
+#include "tp_logits_two.cuh"
 
 namespace tp {
 namespace rows {
 
-constexpr int kThreads = 256;  // per CTA of every kernel here
+constexpr int kThreads = 256;  // per CTA, but of the kernel for long rows
 constexpr int kUnroll = 4;     // 16-byte vectors a thread has in flight
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr double kLn2 = 0.69314718055994530942;
+constexpr float kLn2 = 0.69314718f;
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 __device__ __forceinline__ float ex2(float x) { return ExpTraits<float>::bexp(x); }
@@ -39,6 +40,16 @@ struct Elem<float> {
     static constexpr int kVec = 4;  // elements of a 16-byte vector
     __device__ __forceinline__ static float get(float v) { return v; }
     __device__ __forceinline__ static float put(float v) { return v; }
+    __device__ __forceinline__ static uint4 none() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
+    template <int N>
+    __device__ __forceinline__ static float top(const uint4 (&r)[N]) {
+        float m = neg_inf();
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+            m = max_nan(max_nan(m, max_nan(__uint_as_float(r[u].x), __uint_as_float(r[u].y))),
+                        max_nan(__uint_as_float(r[u].z), __uint_as_float(r[u].w)));
+        return m;
+    }
     __device__ __forceinline__ static uint4 pack(const float* f) {
         return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
     }
@@ -50,6 +61,17 @@ template <>
 struct Elem<__half> {
     static constexpr int kVec = 8;
     __device__ __forceinline__ static float get(__half v) { return __half2float(v); }
+    __device__ __forceinline__ static uint4 none() { return make_uint4(0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u); }
+    // largest element, two at a time; NaN if there is one
+    template <int N>
+    __device__ __forceinline__ static float top(const uint4 (&r)[N]) {
+        __half2 m = of(r[0].x);
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+            m = __hmax2_nan(__hmax2_nan(m, __hmax2_nan(of(r[u].x), of(r[u].y))), __hmax2_nan(of(r[u].z), of(r[u].w)));
+        return max_nan(__half2float(__low2half(m)), __half2float(__high2half(m)));
+    }
+    __device__ __forceinline__ static __half2 of(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
     __device__ __forceinline__ static __half put(float v) { return __float2half_rn(v); }
     __device__ __forceinline__ static uint32_t two(float a, float b) {
         const __half2 h = __floats2half2_rn(a, b);
@@ -70,6 +92,17 @@ template <>
 struct Elem<__nv_bfloat16> {
     static constexpr int kVec = 8;
     __device__ __forceinline__ static float get(__nv_bfloat16 v) { return __bfloat162float(v); }
+    __device__ __forceinline__ static uint4 none() { return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
+    // largest element, two at a time; NaN if there is one
+    template <int N>
+    __device__ __forceinline__ static float top(const uint4 (&r)[N]) {
+        __nv_bfloat162 m = of(r[0].x);
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+            m = __hmax2_nan(__hmax2_nan(m, __hmax2_nan(of(r[u].x), of(r[u].y))), __hmax2_nan(of(r[u].z), of(r[u].w)));
+        return max_nan(__bfloat162float(__low2bfloat16(m)), __bfloat162float(__high2bfloat16(m)));
+    }
+    __device__ __forceinline__ static __nv_bfloat162 of(uint32_t u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); }
     __device__ __forceinline__ static __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
     __device__ __forceinline__ static uint32_t two(float a, float b) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -93,26 +126,45 @@ __device__ __forceinline__ T* row_at(const View& r, int64_t i) {
 }
 
 // A row as 16-byte vectors: vector j covers elements j V - off .. j V - off + V - 1, where off is the row's
-// distance from the 16-byte boundary below it. Vectors that lie inside the row are read at once; the first
-// and the last may hang over it and are read element by element, with -inf outside.
+// distance from the 16-byte boundary below it. The first and the last may hang over the row's ends: those are
+// read element by element, with -inf outside. (M <= 2^30, so every index fits 32 bits.)
 template <class T>
 struct RowVecs {
     static constexpr int V = Elem<T>::kVec;
     const T* p;
+    const uint4* base;  // the boundary below the row
     int off, M, n;
+    int lo, hi;  // vectors lo .. hi - 1 lie inside the row
     __device__ __forceinline__ RowVecs(const T* row, int M_) : p(row), M(M_) {
         off = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
-        n = (int)(((int64_t)M + off + V - 1) / V);
+        base = reinterpret_cast<const uint4*>(row - off);
+        n = (M + off + V - 1) / V;
+        lo = off ? 1 : 0, hi = (M + off) / V;
     }
-    __device__ __forceinline__ int64_t first(int j) const { return (int64_t)j * V - off; }
-    // vectors j0 .. j1 - 1 all lie inside the row
-    __device__ __forceinline__ bool inside(int j0, int j1) const { return first(j0) >= 0 && first(j1) <= M; }
-    __device__ __forceinline__ const uint4* at(int j) const { return reinterpret_cast<const uint4*>(p + first(j)); }
-    __device__ __forceinline__ uint4 raw(int j) const { return __ldg(at(j)); }
-    __device__ __forceinline__ void edge(int j, float* f) const {
-        const int64_t e = first(j);
+    __device__ __forceinline__ int first(int j) const { return j * V - off; }
+    __device__ __forceinline__ bool inside(int j) const { return j >= lo && j < hi; }
+    __device__ __forceinline__ uint4 edge(int j) const {
+        const int e = first(j);
+        float f[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = (j < n && e + i >= 0 && e + i < M) ? Elem<T>::get(p[e + i]) : neg_inf();
+        for (int i = 0; i < V; ++i) f[i] = (e + i >= 0 && e + i < M) ? Elem<T>::get(p[e + i]) : neg_inf();
+        return Elem<T>::pack(f);
+    }
+    // vectors from + u step, u < N; -inf from `end` on
+    template <int N>
+    __device__ __forceinline__ void load(uint4 (&r)[N], int from, int step, int end) const {
+        if (from >= lo && from + (N - 1) * step < min(end, hi)) {  // no branch between the loads
+#pragma unroll
+            for (int u = 0; u < N; ++u) r[u] = __ldcg(base + from + u * step);
+            return;
+        }
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const int j = from + u * step;
+            if (j < end && inside(j)) r[u] = __ldcg(base + j);
+            else if (j < end) r[u] = edge(j);
+            else r[u] = Elem<T>::none();
+        }
     }
 };
 
@@ -125,10 +177,10 @@ __device__ __forceinline__ uint4 window(const uint4& a, const uint4& b, int shif
     return make_uint4(__funnelshift_r(w0, w1, r), __funnelshift_r(w1, w2, r), __funnelshift_r(w2, w3, r), __funnelshift_r(w3, w4, r));
 }
 
-// The threads that share a row: a warp (several rows a CTA), or the CTA. kThreads threads a CTA either way.
+// The threads that share a row: a warp (kThreads / 32 rows a CTA), or a CTA of TEAM threads.
 template <int TEAM>
 struct Team {
-    static constexpr int kPerCta = kThreads / TEAM;
+    static constexpr int kPerCta = TEAM == 32 ? kThreads / 32 : 1;
     static constexpr bool kWarp = TEAM == 32;
     __device__ __forceinline__ static int id() { return kWarp ? threadIdx.x >> 5 : 0; }
     __device__ __forceinline__ static int tid() { return kWarp ? threadIdx.x & 31 : threadIdx.x; }
@@ -208,25 +260,82 @@ struct State {
     }
 };
 
-// n scores into the state.
-template <int N>
-__device__ __forceinline__ void add_scores(State& st, const float (&f)[N], float c) {
-    float top = f[0];
-#pragma unroll
-    for (int i = 1; i < N; ++i) top = max_nan(top, f[i]);
-    top = max_nan(top, st.m);
+// Two fp32 values in one register pair: one instruction for both.
+__device__ __forceinline__ float2 sub2(float2 a, float b) {
+    float2 r;
+    const float2 m = make_float2(-b, -b);
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(m)));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float b) {
+    float2 r;
+    const float2 m = make_float2(b, b);
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(m)));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
+          "l"(reinterpret_cast<const uint64_t&>(c)));
+    return r;
+}
+
+// N vectors of scores into the state. About nine instructions for two scores: unpack, x - m, the product with c,
+// two ex2, the sums s and h, half a maximum each. A masked score (-inf) makes 0 x inf of its term of h: a sum h
+// that comes out NaN is formed again with the distance bounded, and so are later ones of the thread (`careful`).
+template <class T, int N>
+__device__ __forceinline__ void add_scores(State& st, const uint4 (&r)[N], float c, bool& careful) {
+    constexpr int V = Elem<T>::kVec;
+    const float top = max_nan(Elem<T>::top(r), st.m);
     if (top == neg_inf()) return;
     st.raise(top, c);
-    float s[4] = {0.f, 0.f, 0.f, 0.f}, h[4] = {0.f, 0.f, 0.f, 0.f};
+    float2 s[2], h[2];
+    if (!careful) {
+        s[0] = s[1] = h[0] = h[1] = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const float d = max_nan(f[i] - top, -1e30f);  // -inf (masked): weight 0 times a finite distance
-        const float e = ex2(d * c);
-        s[i & 3] += e;
-        h[i & 3] = fmaf(e, d, h[i & 3]);
+        for (int u = 0; u < N; ++u) {
+            float f[V];
+            Elem<T>::unpack(r[u], f);
+#pragma unroll
+            for (int i = 0; i < V; i += 2) {
+                const float2 d = sub2(make_float2(f[i], f[i + 1]), top), x = mul2(d, c);
+                const float2 e = make_float2(ex2(x.x), ex2(x.y));
+                s[i / 2 & 1] = add2(s[i / 2 & 1], e), h[i / 2 & 1] = fma2(e, d, h[i / 2 & 1]);
+            }
+        }
+        h[0] = add2(h[0], h[1]);
+        careful = !(h[0].x + h[0].y <= 0.f);
     }
-    st.add((s[0] + s[1]) + (s[2] + s[3]));
-    st.h += (h[0] + h[1]) + (h[2] + h[3]);
+    if (careful) {
+        s[0] = s[1] = h[0] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            float f[V];
+            Elem<T>::unpack(r[u], f);
+#pragma unroll
+            for (int i = 0; i < V; i += 2) {
+                const float2 d = make_float2(max_nan(f[i] - top, -1e30f), max_nan(f[i + 1] - top, -1e30f));
+                const float2 e = make_float2(ex2(d.x * c), ex2(d.y * c));
+                s[i / 2 & 1] = add2(s[i / 2 & 1], e), h[0] = fma2(e, d, h[0]);
+            }
+        }
+    }
+    const float2 sum = add2(s[0], s[1]);
+    st.add(sum.x + sum.y);
+    st.h += h[0].x + h[0].y;
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -246,7 +355,7 @@ __device__ __forceinline__ void warp_sum(State& st) {
 }
 
 struct ReduceBuf {
-    float m[kThreads / 32], s[kThreads / 32], lo[kThreads / 32], h[kThreads / 32];
+    float m[32], s[32], lo[32], h[32];
 };
 
 // The state of all scores of the team, in every thread. A CTA's takes two barriers; the buffer may be used
@@ -297,38 +406,46 @@ __device__ __forceinline__ State cluster_merge(const ClusterBuf& b, int size, fl
     return all;
 }
 
-// c is rounded: the sum's first-order correction to the exact 1/T (see Scale in tp_logits_args.h)
-__device__ __forceinline__ double exact_sum(const State& st, const Scale& sc) {
-    return (double)st.s + ((double)st.lo + (double)sc.delta * st.h);
+// The sum of a state, corrected for the rounding of c (Scale in tp_logits_args.h).
+__device__ __forceinline__ Two exact_sum(const State& st, const Scale& sc) {
+    return two_sum(st.s, st.lo + sc.delta * st.h);
 }
 
-// ln z for z >= 2^-120 in fp64: an fp32 logarithm and one correction through the fp64 exponential,
-// ln z = l + ln(z e^-l) with z e^-l within 1e-6 of 1. About 18 fp64 operations; the pipe has 2 lanes a clock.
-__device__ __forceinline__ double ln64(double z) {
-    const double l = (double)logf((float)z);
-    const double r = fma(z, exp_table(-l), -1.0);
-    return l + fma(-0.5 * r, r, r);
-}
-
-__device__ __forceinline__ double warp_sum64(double v) {
+// r with the elements whose bits are set masked (few vectors have any)
+template <class T>
+__device__ __forceinline__ uint4 without(const uint4& r, uint32_t bits) {
+    constexpr int V = Elem<T>::kVec;
+    if (!(bits & ((1u << V) - 1))) return r;
+    float f[V];
+    Elem<T>::unpack(r, f);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-    return v;
+    for (int i = 0; i < V; ++i)
+        if (bits & (1u << i)) f[i] = neg_inf();
+    return Elem<T>::pack(f);
 }
+
+// What a row's loss takes from the list alone. lm is the largest listed score (0 if all are -inf).
+struct ListSums {
+    Two Z;     // sum q
+    Two zl;    // rest: sum over the listed columns, each once, of exp((x - lm)/T)
+    Two q_r_ln;
+    float q_r, lm;
+};
 
 // A teacher's list of one row in shared memory.
 struct ListBuf {
-    int id[kMaxList];
+    alignas(16) int id[kMaxList];    // -1: the entry does not count
     float y[kMaxList], x[kMaxList];  // the teacher's value, the row's score
     float q[kMaxList];               // the teacher's share
+    float2 u[kMaxList];              // log q - (x - lm)/T, two words
+    ListSums sums;
     unsigned char first[kMaxList];   // no earlier entry has its column
     __device__ __forceinline__ bool ok(int k) const { return id[k] >= 0; }
 };
 
-// Loads the list of a row whose scores start at p; false when no entry counts. Scores are read of the columns
-// from e0 to e1 only (what another CTA may be overwriting is its own to read). Ends with a barrier.
-template <class T, int TEAM>
-__device__ __forceinline__ bool load_list(const DistillArgs& a, int64_t row, const T* p, ListBuf& l, int64_t e0, int64_t e1) {
+// Loads a row's list; false when no entry counts. Ends with a barrier.
+template <int TEAM>
+__device__ __forceinline__ bool load_list(const DistillArgs& a, int64_t row, ListBuf& l) {
     bool some = false;
     for (int k = Team<TEAM>::tid(); k < a.K; k += TEAM) {
         const int64_t id = a.ids[row * a.K + k];
@@ -336,26 +453,134 @@ __device__ __forceinline__ bool load_list(const DistillArgs& a, int64_t row, con
         const bool ok = id >= 0 && id < a.x.M && !(y == neg_inf());
         l.id[k] = ok ? (int)id : -1;
         l.y[k] = y;
-        l.x[k] = ok && id >= e0 && id < e1 ? Elem<T>::get(p[id]) : 0.f;
         some |= ok;
     }
     if (!Team<TEAM>::any(some)) return false;
     Team<TEAM>::sync();
     return true;
 }
-// Marks the first entry of each column; true when a column is listed twice. Ends with a barrier.
-template <int TEAM>
-__device__ __forceinline__ bool mark_first(ListBuf& l, int K) {
+// Scores of the listed columns from e0 to e1 (what another CTA may be overwriting is its own to read) of the row
+// at p, and the first entry of each column; true when a column is listed twice. Ends with a barrier.
+template <class T, int TEAM>
+__device__ __forceinline__ bool look_up(const DistillArgs& a, const T* p, ListBuf& l, int e0, int e1) {
     bool twice = false;
-    for (int k = Team<TEAM>::tid(); k < K; k += TEAM) {
+    for (int k = Team<TEAM>::tid(); k < a.K; k += TEAM) {
+        const int id = l.id[k];
+        const float x = id >= e0 && id < e1 && id >= 0 ? Elem<T>::get(p[id]) : 0.f;
         bool first = true;
-        for (int j = 0; j < k; ++j) first &= l.id[j] != l.id[k];
+        int j = 0;
+        for (; j + 4 <= k; j += 4) {
+            const int4 v = *reinterpret_cast<const int4*>(l.id + j);
+            first &= v.x != id && v.y != id && v.z != id && v.w != id;
+        }
+        for (; j < k; ++j) first &= l.id[j] != id;
         l.first[k] = first;
-        twice |= !first && l.ok(k);
+        twice |= !first && id >= 0;
+        l.x[k] = x;
     }
     twice = Team<TEAM>::any(twice);
     Team<TEAM>::sync();
     return twice;
+}
+
+// (x - m)/T; one word where it is -inf, or as good as
+__device__ __forceinline__ Two over_T(float x, float m, const Scale& sc) {
+    const float d = x - m;
+    if (!(d > -1e30f)) return Two{d * sc.inv, 0.f};
+    return mul(two_sum(x, -m), Two{sc.inv, sc.inv_lo});
+}
+
+// By one warp; leaves the shares in l.q and l.u, the rest in l.sums (in shared memory: the row is read in between,
+// and its loop needs the registers).
+__device__ __forceinline__ void sum_list(const DistillArgs& a, ListBuf& l) {
+    const int lane = threadIdx.x & 31;
+    ListSums r;
+    float lm = neg_inf(), ym = neg_inf();
+    for (int k = lane; k < a.K; k += 32)
+        if (l.ok(k)) lm = max_nan(lm, l.x[k]), ym = max_nan(ym, l.y[k]);
+    lm = warp_max(lm);
+    if (lm == neg_inf()) lm = 0.f;
+    if (!a.rest) ym = warp_max(ym);
+    Two sum{0.f, 0.f}, zl{0.f, 0.f};
+    for (int k = lane; k < a.K; k += 32) {
+        if (!l.ok(k)) {
+            l.q[k] = 0.f;
+            continue;
+        }
+        const Two lq = a.rest ? Two{l.y[k], 0.f} : over_T(l.y[k], ym, a.sc), d = over_T(l.x[k], lm, a.sc), q = exp_two(lq);
+        sum = add(sum, q);
+        if (a.rest && l.first[k]) zl = add(zl, exp_two(d));
+        l.q[k] = q.h;
+        const Two u = d.h == neg_inf() ? Two{-d.h, 0.f} : add(lq, neg(d));
+        l.u[k] = make_float2(u.h, u.l);
+    }
+    sum = warp_add(sum);
+    r.Z = sum, r.lm = lm, r.zl = Two{0.f, 0.f}, r.q_r_ln = Two{0.f, 0.f}, r.q_r = 0.f;
+    if (a.rest) {
+        r.zl = warp_add(zl);
+        const Two left = add(Two{1.f, 0.f}, neg(sum));
+        if (left.h >= kLeastRest) r.q_r = left.h, r.q_r_ln = ln_two(left);
+    } else {
+        const Two ln = neg(ln_two(sum));
+        const float scale = 1.f / sum.h;
+        for (int k = lane; k < a.K; k += 32) {
+            const Two u = add(Two{l.u[k].x, l.u[k].y}, ln);
+            l.q[k] *= scale;
+            if (l.u[k].x < __int_as_float(0x7f800000)) l.u[k] = make_float2(u.h, u.l);
+        }
+        r.Z = Two{1.f, 0.f};
+    }
+    if (lane == 0) l.sums = r;
+    __syncwarp();
+}
+
+// Unlisted columns are told by a bit map of this many columns of the row at a time.
+template <int TEAM>
+struct Marks {
+    static constexpr int kCols = TEAM == 32 ? 1 << 12 : 1 << 18;
+    alignas(16) uint32_t bits[kCols / 32];
+    // bit i < n of the map becomes: element e0 + i is listed. Barriers on both sides.
+    __device__ __forceinline__ void set(const ListBuf& l, int K, int e0, int n) {
+        Team<TEAM>::sync();
+        for (int i = Team<TEAM>::tid(); i < (n + 127) / 128; i += TEAM) reinterpret_cast<uint4*>(bits)[i] = make_uint4(0, 0, 0, 0);
+        Team<TEAM>::sync();
+        for (int k = Team<TEAM>::tid(); k < K; k += TEAM) {
+            const int at = l.ok(k) ? l.id[k] - e0 : -1;
+            if (at >= 0 && at < n) atomicOr(&bits[at >> 5], 1u << (at & 31));
+        }
+        Team<TEAM>::sync();
+    }
+};
+
+// The thread's state of the slice's columns; of the unlisted ones where REST.
+template <class T, int TEAM, bool REST>
+__device__ __forceinline__ State read_slice(const DistillArgs& a, const RowVecs<T>& x, const Slice& sl, const ListBuf& list,
+                                            Marks<TEAM>& marks) {
+    constexpr int V = Elem<T>::kVec, kMarkVecs = Marks<TEAM>::kCols / V;
+    const int t = Team<TEAM>::tid();
+    State st;
+    bool careful = false;
+    for (int part = sl.begin; part < sl.end; part += REST ? kMarkVecs : sl.end) {
+        const int end = REST ? min(sl.end, part + kMarkVecs) : sl.end;
+        uint4 next[kUnroll];  // a chunk is under way while the one before it is reduced
+        x.load(next, part + t, TEAM, end);
+        if (REST) marks.set(list, a.K, x.first(part), (end - part) * V);
+        for (int base = part; base < end; base += TEAM * kUnroll) {
+            uint4 r[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) r[u] = next[u];
+            x.load(next, base + TEAM * kUnroll + t, TEAM, end);
+            if (REST) {
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) {
+                    const int bit = (base - part + u * TEAM + t) * V & (Marks<TEAM>::kCols - 1);
+                    r[u] = without<T>(r[u], marks.bits[bit >> 5] >> (bit & 31));
+                }
+            }
+            add_scores<T>(st, r, a.sc.c, careful);
+        }
+    }
+    return st;
 }
 
 struct RowStats {
@@ -366,80 +591,43 @@ struct RowStats {
     float coef;     // gradient of a column that is not listed: coef exp((x - gm)/T - gls) / T
 };
 
-// The list's part of a row, by one warp: the teacher's shares q (left in l.q), the loss, and what the gradient
-// takes. `st` is the state of all columns, or of the unlisted ones (rest; l.first and every l.x are then
-// read). In fp64: what is left of a loss near zero is the difference of logarithms that agree to several digits.
-__device__ __forceinline__ RowStats distill_row(const DistillArgs& a, const State& st, ListBuf& l) {
-    const int lane = threadIdx.x & 31;
-    const double inv = a.sc.inv64;
-    const double zs = exact_sum(st, a.sc);
+// The row's loss and what its gradient takes, by the warp that summed the list. `st` is the state of all columns,
+// or of the unlisted ones (rest).
+__device__ __forceinline__ RowStats close_row(const DistillArgs& a, const State& st, const ListBuf& b) {
+    const ListSums& l = b.sums;
+    const Two zs = exact_sum(st, a.sc);
     float m = st.m;  // maximum over all columns
-    double z = zs;   // sum over all columns, relative to m
-    double q[4], lq[4];
-    if (a.rest) {
-        float lm = neg_inf();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int k = lane + 32 * j;
-            if (k < a.K && l.ok(k)) lm = max_nan(lm, l.x[k]);
-        }
-        m = max_nan(st.m, warp_max(lm));
-        double sum = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int k = lane + 32 * j;
-            const bool ok = k < a.K && l.ok(k);
-            lq[j] = ok ? l.y[k] : 0.0;
-            q[j] = ok ? exp_table(lq[j]) : 0.0;
-            if (ok && l.first[k] && l.x[k] > neg_inf()) sum += exp_table(((double)l.x[k] - m) * inv);
-        }
-        z = warp_sum64(sum);
-        if (st.m > neg_inf()) z += zs * exp_table(((double)st.m - m) * inv);
-        if (m != m) z = m;  // NaN
-    } else {
-        float ym = neg_inf();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int k = lane + 32 * j;
-            if (k < a.K && l.ok(k)) ym = max_nan(ym, l.y[k]);
-        }
-        ym = warp_max(ym);
-        double sum = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int k = lane + 32 * j;
-            const bool ok = k < a.K && l.ok(k);
-            lq[j] = ok ? ((double)l.y[k] - ym) * inv : 0.0;
-            q[j] = ok ? exp_table(lq[j]) : 0.0;
-            sum += q[j];
-        }
-        sum = warp_sum64(sum);
-        const double ln = ln64(sum), r = 1.0 / sum;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) q[j] *= r, lq[j] -= ln;
+    Two z = zs;      // sum over all columns, relative to m
+    if (a.rest && l.zl.h > 0.f) {
+        m = max_nan(st.m, l.lm);
+        z = mul(l.zl, exp_two(over_T(l.lm, m, a.sc)));
+        if (st.m != neg_inf()) z = add(z, mul(zs, exp_two(over_T(st.m, m, a.sc))));
     }
-    const double m0 = m == neg_inf() ? 0.0 : (double)m, ls = m == neg_inf() ? 0.0 : ln64(z);
-    double loss = 0, Z = 0;
+    const bool some = m != neg_inf();
+    const Two ls = some ? ln_two(z) : Two{0.f, 0.f};
+    // sum q (log q - (x - lm)/T + c), c = ln z - (lm - m)/T
+    const Two c = add(ls, neg(over_T(l.lm, some ? m : 0.f, a.sc)));
+    float loss = 0.f;
+    for (int k = threadIdx.x & 31; k < a.K; k += 32)
+        if (b.q[k] > 0.f) {
+            const Two u{b.u[k].x, b.u[k].y};
+            loss += b.q[k] * (u.h < __int_as_float(0x7f800000) ? add(u, c).h : u.h);
+        }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int k = lane + 32 * j;
-        if (q[j] > 0) loss += q[j] * (lq[j] - (((double)l.x[k] - m0) * inv - ls));
-        Z += q[j];
-        if (k < a.K) l.q[k] = (float)q[j];
-    }
-    loss = warp_sum64(loss), Z = warp_sum64(Z);
+    for (int o = 16; o; o >>= 1) loss += __shfl_xor_sync(~0u, loss, o);
     RowStats s;
-    s.m = s.gm = m, s.ls = s.gls = (float)ls, s.coef = (float)Z;
+    s.m = s.gm = m, s.ls = s.gls = ls.h, s.coef = l.Z.h, s.Z = l.Z.h;
     if (a.rest) {
         s.coef = 0.f;
         if (st.m != neg_inf()) {
-            const double q_r = 1.0 - Z >= kLeastRest ? 1.0 - Z : 0.0, lr = ln64(zs), lp = ((double)st.m - m0) * inv + lr - ls;
-            if (q_r > 0) loss += q_r * (ln64(q_r) - lp);
-            Z += q_r;
-            s.gm = st.m, s.gls = (float)lr, s.coef = (float)(Z * exp_table(lp) - q_r);
+            const Two lr = ln_two(zs), lp = add(add(over_T(st.m, m, a.sc), lr), neg(ls));  // log p_r
+            if (l.q_r > 0.f) loss += l.q_r * add(l.q_r_ln, neg(lp)).h;
+            const Two Z = add(l.Z, Two{l.q_r, 0.f});
+            s.gm = st.m, s.gls = lr.h, s.Z = Z.h, s.coef = add(mul(Z, exp_two(lp)), Two{-l.q_r, 0.f}).h;
         }
     }
-    s.Z = (float)Z, s.loss = (float)loss;
+    if (m != m) loss = m;
+    s.loss = loss;
     return s;
 }
 

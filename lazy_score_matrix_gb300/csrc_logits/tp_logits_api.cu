@@ -46,7 +46,7 @@ tp_status check_rows(const tp_rows* r, const char* name, bool written) {
     if (r->dtype != TP_ROWS_F32 && r->dtype != TP_ROWS_F16 && r->dtype != TP_ROWS_BF16)
         return invalid(n + ": dtype must be TP_ROWS_F32, TP_ROWS_F16 or TP_ROWS_BF16");
     constexpr int64_t lim = int64_t(1) << 31;
-    if (r->N < 1 || r->M < 1 || r->N >= lim || r->M >= lim) return invalid(n + ": N and M must be in [1, 2^31)");
+    if (r->N < 1 || r->M < 1 || r->N >= lim || r->M > lim / 2) return invalid(n + ": N must be in [1, 2^31) and M in [1, 2^30]");
     if (r->group < 1 || r->group > r->N || r->N % r->group) return invalid(n + ": N must be a multiple of group >= 1");
     const int64_t groups = r->N / r->group;
     const int64_t gs = groups > 1 ? r->group_stride : 0, rs = r->group > 1 ? r->row_stride : 0;
@@ -119,10 +119,11 @@ View view(const tp_rows* r) {
 
 Scale scale_of(double t) {
     Scale s;
-    s.inv64 = 1.0 / t;
-    s.inv = (float)s.inv64;
+    const double inv = 1.0 / t;
+    s.inv = (float)inv;
+    s.inv_lo = (float)(inv - (double)s.inv);
     s.c = (float)(1.4426950408889634074 / t);
-    s.delta = (float)(s.inv64 - (double)s.c * 0.69314718055994530942);
+    s.delta = (float)(inv - (double)s.c * 0.69314718055994530942);
     return s;
 }
 
@@ -297,10 +298,8 @@ tp_status tp_topk_distillation_grad(const tp_rows* x, int K, const int64_t* ids,
         a.weights = weights;
         a.g = view(grad);
         const cudaStream_t s = static_cast<cudaStream_t>(stream);
-        if (launch_distill_grad(x->dtype, a, s)) return launched(1);
-        launch_distill(x->dtype, a, s);  // rows too long to stay on chip
-        launch_distill_backward(x->dtype, a, s);
-        return launched(2);
+        launch_distill_grad(x->dtype, a, s);
+        return launched(1);
     });
 }
 

@@ -14,7 +14,7 @@ constexpr int kMaxList = 128;  // longest list of alternatives, and of a teacher
 // The unlisted columns' share 1 - sum q counts as 0 below this: log probabilities rounded to fp32, and a common
 // error of their normaliser of a few 2^-24, leave up to about 1e-6 of a full list, and a student that masks
 // everything else by a large negative score would turn such a remainder into any loss at all.
-constexpr double kLeastRest = 1.0 / (1 << 20);
+constexpr float kLeastRest = 1.f / (1 << 20);
 constexpr int kStats = 8;      // floats per row that a forward leaves for its backward
 
 struct View {
@@ -27,8 +27,7 @@ struct View {
 // delta = 1/T - c ln 2, what the rounding of c takes from the exponent's slope: a sum s of exponentials
 // with first moment h is corrected to s + delta h.
 struct Scale {
-    float c, delta, inv;
-    double inv64;
+    float c, delta, inv, inv_lo;  // inv + inv_lo = 1/T
 };
 
 struct LogprobArgs {
@@ -62,10 +61,12 @@ struct Shape {
     bool warp;
     int cluster;
     unsigned grid;
+    unsigned threads = 256;
     size_t smem = 0;
 };
-constexpr int64_t kWarpCols = 4096, kWarpRows = 152 * 8;
-constexpr int64_t kFewRows = 152 * 4;
+constexpr int64_t kSms = 152;
+constexpr int64_t kWarpCols = 4096, kWarpRows = kSms * 8;
+constexpr int64_t kFewRows = kSms * 4;
 
 // Many rows: one CTA a row, or, where a row is short, one warp a row. Few rows: up to 8 CTAs a row, as long as a
 // CTA keeps a chunk of `chunk` columns of its own.
@@ -82,7 +83,7 @@ template <class... KArgs, class... Args>
 inline void launch(void (*kernel)(KArgs...), const Shape& sh, cudaStream_t s, const Args&... a) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(sh.grid);
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(sh.threads);
     cfg.dynamicSmemBytes = sh.smem;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -97,7 +98,7 @@ inline void launch(void (*kernel)(KArgs...), const Shape& sh, cudaStream_t s, co
 void launch_logprobs(tp_rows_dtype t, const LogprobArgs& a, cudaStream_t s);
 void launch_logprobs_backward(tp_rows_dtype t, const LogprobArgs& a, cudaStream_t s);
 void launch_distill(tp_rows_dtype t, const DistillArgs& a, cudaStream_t s);
-bool launch_distill_grad(tp_rows_dtype t, const DistillArgs& a, cudaStream_t s);  // false: the rows do not fit
+void launch_distill_grad(tp_rows_dtype t, const DistillArgs& a, cudaStream_t s);
 void launch_distill_backward(tp_rows_dtype t, const DistillArgs& a, cudaStream_t s);
 
 }  // namespace rows

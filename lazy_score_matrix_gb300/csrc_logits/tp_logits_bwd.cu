@@ -10,30 +10,6 @@ namespace tp {
 namespace rows {
 namespace {
 
-// The scores of a row in global memory, fetched for 16-byte vectors of the gradient's alignment.
-template <class T>
-struct FromRow {
-    static constexpr int V = Elem<T>::kVec;
-    const T* p;
-    int M;
-    bool match;  // the scores have the gradient's alignment
-    __device__ __forceinline__ FromRow(const T* p_, int M_, const T* o)
-        : p(p_), M(M_), match(((reinterpret_cast<uintptr_t>(p_) ^ reinterpret_cast<uintptr_t>(o)) & 15u) == 0) {}
-    // false: elements e .. e + V - 1 have to be fetched one by one
-    __device__ __forceinline__ bool get(int64_t e, uint4& v) const {
-        if (match) {
-            v = __ldcs(reinterpret_cast<const uint4*>(p + e));  // not .nc: the gradient may overwrite the scores
-            return true;
-        }
-        const int shift = (int)(reinterpret_cast<uintptr_t>(p + e) & 15u), back = shift / (int)sizeof(T);
-        if (e - back < 0 || e - back + 2 * V > M) return false;
-        const uint4* q = reinterpret_cast<const uint4*>(p + (e - back));
-        v = window(q[0], q[1], shift);  // neighbours read the same bytes: cached
-        return true;
-    }
-    __device__ __forceinline__ float one(int64_t e) const { return Elem<T>::get(p[e]); }
-};
-
 // Rows are visited from the last to the first: the forward has read the last ones most recently, and what of
 // them is left in the cache need not come from memory again.
 template <int TEAM>
@@ -55,9 +31,9 @@ __global__ void __launch_bounds__(kThreads) logprobs_bwd_kernel(const LogprobArg
     const float g1 = a.g_logprob ? a.g_logprob[row] * a.sc.inv : 0.f;
     const float g2 = ENTROPY ? a.g_entropy[row] * a.sc.inv : 0.f;
     const float ls2 = ls * kLog2e, c = a.sc.c, gt = a.g_logprob ? g1 : 0.f;
-    const float b1 = fmaf(g2, H, g1), b2 = g2 * (float)kLn2;
-    const FromRow<T> x(row_at<const T>(a.x, row), a.x.M, o);
-    map_range<T, TEAM>(o, r.e0, r.e1, x, [&](float* f, int64_t e) {
+    const float b1 = fmaf(g2, H, g1), b2 = g2 * kLn2;
+    const Source<T> x = from_row<T>(row_at<const T>(a.x, row), a.x.M, o);
+    map_range<T, TEAM, true>(o, r.e0, r.e1, x, [&](float* f, int e) {
 #pragma unroll
         for (int i = 0; i < Elem<T>::kVec; ++i) {
             float t = fmaf(f[i] - m, c, -ls2);  // log2 p
@@ -83,14 +59,14 @@ __global__ void __launch_bounds__(kThreads) distill_bwd_kernel(const DistillArgs
     const T* p = row_at<const T>(a.x, row);
     ListBuf& list = lists[Tm::id()];
     const float* st = a.stats + row * kStats;
-    if (!load_list<T, TEAM>(a, row, p, list, r.e0, r.e1) || st[0] == neg_inf()) return zero_range<T, TEAM>(o, r.e0, r.e1);
-    const bool twice = mark_first<TEAM>(list, a.K);
+    if (!load_list<TEAM>(a, row, list) || st[0] == neg_inf()) return zero_range<T, TEAM>(o, r.e0, r.e1);
+    const bool twice = look_up<T, TEAM>(a, p, list, r.e0, r.e1);
     if (TEAM == 32 || threadIdx.x < 32) shares(a, list);
     Tm::sync();
     RowStats s;
     s.m = st[0], s.ls = st[1], s.gm = st[2], s.gls = st[3], s.Z = st[4], s.coef = st[5];
     const float w = (a.weights ? a.weights[row] : 1.f) * a.sc.inv;
-    distill_row_grad<T, TEAM>(a, s, w, o, r.e0, r.e1, FromRow<T>(p, a.x.M, o));
+    distill_row_grad<T, TEAM, true>(a, s, w, o, r.e0, r.e1, from_row<T>(p, a.x.M, o));
     Tm::sync();
     distill_list_grad<T, TEAM>(a, s, w, o, r.e0, r.e1, list, twice);
 }

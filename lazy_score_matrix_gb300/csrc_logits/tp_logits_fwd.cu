@@ -148,7 +148,7 @@ struct Gather {  // the candidates of a cluster's other CTAs
 };
 
 template <class T, int TEAM, bool TOP>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a) {
+__global__ void __launch_bounds__(kThreads, TOP && TEAM != 32 ? 6 : 4) logprobs_kernel(const LogprobArgs a) {
     constexpr int V = Elem<T>::kVec;
     using Tm = Team<TEAM>;
     __shared__ ReduceBuf red;
@@ -170,29 +170,31 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
     Tops<TEAM> best(tops[TOP ? Tm::id() : 0], a.top);
     if (TOP) best.clear();
     State st;
+    bool careful = false;
+    uint4 next[kUnroll];  // without alternatives, a chunk is under way while the one before it is reduced
+    if (!TOP) x.load(next, sl.begin + t, TEAM, sl.end);
     for (int base = sl.begin; base < sl.end; base += TEAM * kUnroll) {
-        float f[kUnroll * V];
-        if (base + TEAM * kUnroll <= sl.end && x.inside(base, base + TEAM * kUnroll)) {
-            uint4 r[kUnroll];
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) r[u] = x.raw(base + u * TEAM + t);
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) Elem<T>::unpack(r[u], f + u * V);
+        uint4 r[kUnroll];
+        if (TOP) {
+            x.load(r, base + t, TEAM, sl.end);
         } else {
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int j = base + u * TEAM + t;
-                x.edge(j < sl.end ? j : x.n, f + u * V);
-            }
+            for (int u = 0; u < kUnroll; ++u) r[u] = next[u];
+            x.load(next, base + TEAM * kUnroll + t, TEAM, sl.end);
         }
-        add_scores(st, f, a.sc.c);
+        add_scores<T>(st, r, a.sc.c, careful);
         if (TOP) {
             if (base == sl.begin) best.start(st.m, sizeof(T) == 2 ? 1ull << 44 : 1ull << 32);
             const float bar = best.bar(x.first(base));
             uint32_t mask = 0;
 #pragma unroll
-            for (int i = 0; i < kUnroll * V; ++i) mask |= f[i] >= bar ? 1u << i : 0u;
-            const auto col = [&](int i) { return (int)(x.first(base + (i / V) * TEAM + t) + i % V); };
+            for (int u = 0; u < kUnroll; ++u) {
+                float f[V];
+                Elem<T>::unpack(r[u], f);
+#pragma unroll
+                for (int i = 0; i < V; ++i) mask |= f[i] >= bar ? 1u << (u * V + i) : 0u;
+            }
+            const auto col = [&](int i) { return x.first(base + (i / V) * TEAM + t) + i % V; };
             best.offer(mask, col, [&](int i) { return Elem<T>::get(x.p[col(i)]); });
         }
     }
@@ -250,27 +252,8 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a)
     }
 }
 
-// Unlisted columns are told by a bit map of this many columns of the row at a time.
-template <int TEAM>
-struct Marks {
-    static constexpr int kCols = TEAM == 32 ? 1 << 12 : 1 << 16;
-    uint32_t bits[kCols / 32];
-    // bit i of the map becomes: element e0 + i is listed. Barriers on both sides.
-    __device__ __forceinline__ void set(const ListBuf& l, int K, int64_t e0) {
-        Team<TEAM>::sync();
-        for (int i = Team<TEAM>::tid(); i < kCols / 32; i += TEAM) bits[i] = 0;
-        Team<TEAM>::sync();
-        for (int k = Team<TEAM>::tid(); k < K; k += TEAM) {
-            const int64_t at = l.ok(k) ? l.id[k] - e0 : -1;
-            if (at >= 0 && at < kCols) atomicOr(&bits[at >> 5], 1u << (at & 31));
-        }
-        Team<TEAM>::sync();
-    }
-};
-
 template <class T, int TEAM, bool REST>
-__global__ void __launch_bounds__(kThreads) distill_kernel(const DistillArgs a) {
-    constexpr int V = Elem<T>::kVec;
+__global__ void __launch_bounds__(kThreads, 4) distill_kernel(const DistillArgs a) {
     using Tm = Team<TEAM>;
     __shared__ ReduceBuf red;
     __shared__ ClusterBuf parts;
@@ -282,7 +265,7 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillArgs a) 
     const int t = Tm::tid();
     const T* p = row_at<const T>(a.x, row);
     ListBuf& list = lists[Tm::id()];
-    if (!load_list<T, TEAM>(a, row, p, list, 0, a.x.M)) {
+    if (!load_list<TEAM>(a, row, list)) {
         if (rank == 0 && t == 0) {
             a.loss[row] = 0.f;
             if (a.stats)
@@ -293,42 +276,9 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillArgs a) 
     if (size > 1) cluster_arrive();
     const RowVecs<T> x(p, a.x.M);
     const Slice sl = slice_of(x.n, rank, size);
-    constexpr int kMarkVecs = Marks<TEAM>::kCols / V;
-    if (REST) mark_first<TEAM>(list, a.K);
-    State st;
-    for (int part = sl.begin; part < sl.end; part += kMarkVecs) {
-        if (REST) marks[Tm::id()].set(list, a.K, x.first(part));
-        const int end = min(sl.end, part + kMarkVecs);
-        for (int base = part; base < end; base += TEAM * kUnroll) {
-            float f[kUnroll * V];
-            if (base + TEAM * kUnroll <= end && x.inside(base, base + TEAM * kUnroll)) {
-                uint4 r[kUnroll];
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u) r[u] = x.raw(base + u * TEAM + t);
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u) Elem<T>::unpack(r[u], f + u * V);
-            } else {
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    const int j = base + u * TEAM + t;
-                    x.edge(j < end ? j : x.n, f + u * V);
-                }
-            }
-            if (REST) {
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    const int bit = (base - part + u * TEAM + t) * V;
-                    const uint32_t w = marks[Tm::id()].bits[(bit >> 5) & (Marks<TEAM>::kCols / 32 - 1)] >> (bit & 31);
-                    if (w & ((1u << V) - 1)) {
-#pragma unroll
-                        for (int i = 0; i < V; ++i)
-                            if (w & (1u << i)) f[u * V + i] = neg_inf();
-                    }
-                }
-            }
-            add_scores(st, f, a.sc.c);
-        }
-    }
+    look_up<T, TEAM>(a, p, list, 0, a.x.M);
+    if (rank == 0 && (TEAM == 32 || threadIdx.x < 32)) sum_list(a, list);
+    State st = read_slice<T, TEAM, REST>(a, x, sl, list, marks[REST ? Tm::id() : 0]);
     st = team_state<TEAM>(st, a.sc.c, red);
     if (size > 1) {
         cluster_wait();  // every CTA of the cluster runs
@@ -339,7 +289,7 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillArgs a) 
         st = cluster_merge(parts, size, a.sc.c);
     }
     if (TEAM == 32 || threadIdx.x < 32) {
-        const RowStats s = distill_row(a, st, list);
+        const RowStats s = close_row(a, st, list);
         if (t == 0) {
             a.loss[row] = s.loss;
             if (a.stats) {

@@ -30,22 +30,19 @@ __device__ __forceinline__ void copies_wait(int left) {
     else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// The scores of a slice in shared memory (vectors of the scores' alignment), fetched for vectors of the
-// gradient's alignment.
+// The scores of a slice in shared memory: n vectors from element e0 on (of the scores' own alignment).
 template <class T>
-struct FromSlice {
-    static constexpr int V = Elem<T>::kVec;
-    const uint4* buf;
-    int64_t e0;  // element at buf[0]
-    int n;       // vectors
-    __device__ __forceinline__ bool get(int64_t e, uint4& v) const {
-        const int at = (int)(e - e0), j = at / V, shift = (at % V) * (int)sizeof(T);
-        if (at < 0 || j >= n || (shift && j + 1 >= n)) return false;
-        v = shift ? window(buf[j], buf[j + 1], shift) : buf[j];
-        return true;
-    }
-    __device__ __forceinline__ float one(int64_t e) const { return Elem<T>::get(reinterpret_cast<const T*>(buf)[e - e0]); }
-};
+__device__ __forceinline__ Source<T> from_slice(const uint4* buf, int e0, int n, const T* o) {
+    constexpr int V = Elem<T>::kVec;
+    Source<T> s;
+    const int at = -off_of(o) - e0;                    // where the gradient's vector 0 begins, in elements of buf
+    const int r = ((at % V) + V) % V, j = (at - r) / V;
+    s.p = reinterpret_cast<const T*>(buf) - e0;
+    s.q = buf + j;
+    s.shift = r * (int)sizeof(T);
+    s.lo = -j, s.hi = n - j - (r ? 1 : 0);
+    return s;
+}
 
 template <class T, int TEAM, bool REST>
 __global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillArgs a, int room) {
@@ -71,8 +68,8 @@ __global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillArg
     const int n = sl.end - sl.begin;
     // the slice's elements, and the gradient's vectors that hold them (the first and the last may be shared with
     // a neighbouring slice and are then written element by element)
-    const int64_t s0 = x.first(sl.begin), e0 = max(s0, (int64_t)0), e1 = min(x.first(sl.end), (int64_t)a.x.M);
-    if (!load_list<T, TEAM>(a, row, p, list, 0, a.x.M)) {
+    const int s0 = x.first(sl.begin), e0 = max(s0, 0), e1 = min(x.first(sl.end), a.x.M);
+    if (!load_list<TEAM>(a, row, list)) {
         if (rank == 0 && t == 0) {
             a.loss[row] = 0.f;
             for (int i = 0; i < kStats; ++i) a.stats[row * kStats + i] = 0.f;
@@ -85,52 +82,37 @@ __global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillArg
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int j = i + u * TEAM;
-            if (j >= n) break;
-            if (x.inside(sl.begin + j, sl.begin + j + 1)) {
-                copy_async(buf + j, x.at(sl.begin + j));
-            } else {
-                float f[V];
-                x.edge(sl.begin + j, f);
-                buf[j] = Elem<T>::pack(f);
-            }
+            if (j < n && x.inside(sl.begin + j)) copy_async(buf + j, x.base + sl.begin + j);
+            else if (j < n) buf[j] = x.edge(sl.begin + j);
         }
         copies_end();
     }
-    const bool twice = mark_first<TEAM>(list, a.K);
+    // what the list alone decides, while the copies are under way
+    const bool twice = look_up<T, TEAM>(a, p, list, 0, a.x.M);
     if (REST) {
         for (int i = t; i < words; i += TEAM) marks[i] = 0;
         Tm::sync();
         for (int k = t; k < a.K; k += TEAM)
             if (list.ok(k) && list.id[k] >= e0 && list.id[k] < e1) {
-                const int at = (int)(list.id[k] - s0);
+                const int at = list.id[k] - s0;
                 atomicOr(&marks[at >> 5], 1u << (at & 31));
             }
         Tm::sync();
     }
+        if (TEAM == 32 || threadIdx.x < 32) sum_list(a, list);
     State st;
+    bool careful = false;
     int left = (n - t + TEAM * kUnroll - 1) / (TEAM * kUnroll);  // groups of this thread
     for (int i = t; i < n; i += TEAM * kUnroll) {
         copies_wait(--left);
-        float f[kUnroll * V];
+        uint4 r[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int j = i + u * TEAM;
-            if (j < n) {
-                Elem<T>::unpack(buf[j], f + u * V);
-                if (REST) {
-                    const uint32_t w = marks[j * V >> 5] >> (j * V & 31);
-                    if (w & ((1u << V) - 1)) {
-#pragma unroll
-                        for (int k = 0; k < V; ++k)
-                            if (w & (1u << k)) f[u * V + k] = neg_inf();
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < V; ++k) f[u * V + k] = neg_inf();
-            }
+            r[u] = j < n ? buf[j] : Elem<T>::none();
+            if (REST && j < n) r[u] = without<T>(r[u], marks[j * V >> 5] >> (j * V & 31));
         }
-        add_scores(st, f, a.sc.c);
+        add_scores<T>(st, r, a.sc.c, careful);
     }
     st = team_state<TEAM>(st, a.sc.c, red);
     if (size > 1) {
@@ -141,7 +123,7 @@ __global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillArg
         st = cluster_merge(parts, size, a.sc.c);
     }
     RowStats s;
-    if (TEAM == 32 || threadIdx.x < 32) s = distill_row(a, st, list);
+    if (TEAM == 32 || threadIdx.x < 32) s = close_row(a, st, list);
     if (rank == 0 && t == 0) {
         a.loss[row] = s.loss;
         float* q = a.stats + row * kStats;
@@ -156,19 +138,96 @@ __global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillArg
         __syncwarp();
     }
     const float w = (a.weights ? a.weights[row] : 1.f) * a.sc.inv;
-    const FromSlice<T> from{buf, s0, n};
     if (s.m == neg_inf()) {  // a row of -inf alone
         zero_range<T, TEAM>(o, e0, e1);
         return;
     }
-    distill_row_grad<T, TEAM>(a, s, w, o, e0, e1, from);
+    distill_row_grad<T, TEAM, false>(a, s, w, o, e0, e1, from_slice<T>(buf, s0, n, o));
     Tm::sync();
     distill_list_grad<T, TEAM>(a, s, w, o, e0, e1, list, twice);
 }
 
 constexpr size_t kSmemMost = 200 * 1024;     // a CTA's slice at most
 constexpr size_t kSmemThree = 68 * 1024;     // three CTAs an SM
+constexpr int64_t kManyRows = 2 * kSms;
 constexpr int64_t kWarpBytes = 4096;         // rows up to this long: one warp a row
+
+// Lets a kernel use so many bytes of dynamic shared memory; `ready` remembers the devices where it may, bit by
+// bit. An error is left for the launch check.
+template <class K>
+bool raise_smem(K kernel, size_t bytes, std::atomic<uint64_t>& ready) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (ready.load(std::memory_order_relaxed) & bit) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
+
+// Rows too long for that, or for enough of them on an SM: one CTA a row reads it twice, and the second time it comes
+// from the L2 cache, as long as the rows under way on the whole card fit there (go_long).
+constexpr int kLongThreads = 512;
+
+template <class T, bool REST>
+__global__ void __launch_bounds__(kLongThreads, 2) distill_grad_long_kernel(const DistillArgs a) {
+    constexpr int TEAM = kLongThreads;
+    __shared__ ReduceBuf red;
+    __shared__ ListBuf list;
+    __shared__ RowStats shared_stats;
+    __shared__ Marks<TEAM> marks[1];
+    const int64_t row = blockIdx.x;
+    const T* p = row_at<const T>(a.x, row);
+    T* o = row_at<T>(a.g, row);
+    const int M = a.x.M;
+    if (!load_list<TEAM>(a, row, list)) {
+        if (threadIdx.x == 0) {
+            a.loss[row] = 0.f;
+            for (int i = 0; i < kStats; ++i) a.stats[row * kStats + i] = 0.f;
+        }
+        return zero_range<T, TEAM>(o, 0, M);
+    }
+    const bool twice = look_up<T, TEAM>(a, p, list, 0, M);
+    if (threadIdx.x < 32) sum_list(a, list);
+    const RowVecs<T> x(p, M);
+    State st = read_slice<T, TEAM, REST>(a, x, Slice{0, x.n}, list, marks[0]);
+    st = team_state<TEAM>(st, a.sc.c, red);
+    if (threadIdx.x < 32) {
+        const RowStats s = close_row(a, st, list);
+        if (threadIdx.x == 0) {
+            shared_stats = s;
+            a.loss[row] = s.loss;
+            float* q = a.stats + row * kStats;
+            q[0] = s.m, q[1] = s.ls, q[2] = s.gm, q[3] = s.gls, q[4] = s.Z, q[5] = s.coef;
+            q[6] = q[7] = 0.f;
+        }
+    }
+    __syncthreads();
+    const RowStats s = shared_stats;
+    if (s.m == neg_inf()) return zero_range<T, TEAM>(o, 0, M);  // a row of -inf alone
+    const float w = (a.weights ? a.weights[row] : 1.f) * a.sc.inv;
+    distill_row_grad<T, TEAM, true>(a, s, w, o, 0, M, from_row<T>(p, M, o));
+    __syncthreads();
+    distill_list_grad<T, TEAM>(a, s, w, o, 0, M, list, twice);
+}
+
+constexpr int64_t kCacheBytes = (int64_t)110 << 20;  // of rows under way, to be found in L2 again
+constexpr size_t kAlone = 120 * 1024;  // dynamic shared memory of which two do not fit an SM
+template <class T, bool REST>
+void go_long(const DistillArgs& a, cudaStream_t s) {
+    auto kernel = distill_grad_long_kernel<T, REST>;
+    static std::atomic<uint64_t> ready{0};
+    if (!raise_smem(kernel, kAlone, ready)) return;
+    Shape sh;
+    sh.warp = false;
+    sh.cluster = 1;
+    sh.threads = kLongThreads;
+    sh.grid = (unsigned)a.N;
+    // two CTAs an SM by their registers, or one by its shared memory
+    sh.smem = 2 * kSms * (int64_t)a.x.M * (int64_t)sizeof(T) <= kCacheBytes ? 0 : kAlone;
+    HookScope h("topk_distillation_grad", s);
+    launch(kernel, sh, s, a);
+}
 
 // Shared memory for slices of n vectors; room receives the vectors per team.
 inline size_t smem_of(int64_t n, int teams, int V, bool rest, int& room) {
@@ -180,20 +239,14 @@ inline size_t smem_of(int64_t n, int teams, int V, bool rest, int& room) {
 template <class T, int TEAM, bool REST>
 void go(const DistillArgs& a, const Shape& sh, int room, cudaStream_t s) {
     auto kernel = distill_grad_kernel<T, TEAM, REST>;
-    static std::atomic<uint64_t> ready{0};  // devices whose limit is raised, bit by bit
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return;
-    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-    if (!(ready.load(std::memory_order_relaxed) & bit)) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMost) != cudaSuccess) return;
-        ready.fetch_or(bit, std::memory_order_relaxed);
-    }
+    static std::atomic<uint64_t> ready{0};
+    if (!raise_smem(kernel, kSmemMost, ready)) return;
     HookScope h("topk_distillation_grad", s);
     launch(kernel, sh, s, a, room);
 }
 
 template <class T>
-bool run(const DistillArgs& a, cudaStream_t s) {
+void run(const DistillArgs& a, cudaStream_t s) {
     constexpr int V = Elem<T>::kVec;
     const int64_t n = ((int64_t)a.x.M + 2 * V - 2) / V + 1;  // vectors of a row at any alignment, at most
     Shape sh;
@@ -205,25 +258,33 @@ bool run(const DistillArgs& a, cudaStream_t s) {
         sh.grid = (unsigned)((a.N + 7) / 8);
         if (a.rest) go<T, 32, true>(a, sh, room, s);
         else go<T, 32, false>(a, sh, room, s);
-        return true;
+        return;
     }
     const auto smem = [&](int c) { return smem_of((n + c - 1) / c, 1, V, a.rest, room); };
-    while (sh.cluster < kMaxCluster && smem(sh.cluster) > kSmemThree) ++sh.cluster;
-    while (sh.cluster < kMaxCluster && a.N * sh.cluster < kFewRows && n >= (int64_t)(sh.cluster + 1) * kThreads) ++sh.cluster;
+    if (a.N >= kManyRows && smem(1) > kSmemThree) {
+        if (a.rest) go_long<T, true>(a, s);
+        else go_long<T, false>(a, s);
+        return;
+    }
+    while (sh.cluster < kMaxCluster && (smem(sh.cluster) > kSmemThree || (a.N * sh.cluster < kFewRows && n >= (int64_t)(sh.cluster + 1) * kThreads)))
+        ++sh.cluster;
     sh.smem = smem(sh.cluster);
-    if (sh.smem > kSmemMost) return false;
+    if (sh.smem > kSmemMost) {
+        if (a.rest) go_long<T, true>(a, s);
+        else go_long<T, false>(a, s);
+        return;
+    }
     sh.grid = (unsigned)(a.N * sh.cluster);
     if (a.rest) go<T, kThreads, true>(a, sh, room, s);
     else go<T, kThreads, false>(a, sh, room, s);
-    return true;
 }
 
 }  // namespace
 
-bool launch_distill_grad(tp_rows_dtype t, const DistillArgs& a, cudaStream_t s) {
-    if (t == TP_ROWS_F32) return run<float>(a, s);
-    if (t == TP_ROWS_F16) return run<__half>(a, s);
-    return run<__nv_bfloat16>(a, s);
+void launch_distill_grad(tp_rows_dtype t, const DistillArgs& a, cudaStream_t s) {
+    if (t == TP_ROWS_F32) run<float>(a, s);
+    else if (t == TP_ROWS_F16) run<__half>(a, s);
+    else run<__nv_bfloat16>(a, s);
 }
 
 }  // namespace rows

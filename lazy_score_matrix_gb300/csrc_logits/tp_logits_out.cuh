@@ -13,76 +13,103 @@ __device__ __forceinline__ int off_of(const T* o) {
 }
 template <class T>
 __device__ __forceinline__ int vecs_of(const T* o, int M) {
-    constexpr int V = Elem<T>::kVec;
-    return (int)(((int64_t)M + off_of(o) + V - 1) / V);
+    return (M + off_of(o) + Elem<T>::kVec - 1) / Elem<T>::kVec;
 }
 template <class T>
-__device__ __forceinline__ int64_t first_of(const T* o, int j) {
-    return (int64_t)j * Elem<T>::kVec - off_of(o);
+__device__ __forceinline__ int first_of(const T* o, int j) {
+    return j * Elem<T>::kVec - off_of(o);
 }
 
-// o[e] = f(score e) for e0 <= e < e1. from.get(e, v) fetches V adjacent scores, or declines; from.one(e) fetches
-// one. f(float[V], e) turns the scores of e .. e + V - 1 into gradients. A vector that e0 or e1 cuts is written
-// element by element: what lies beyond may be another CTA's.
-template <class T, int TEAM, class From, class F>
-__device__ __forceinline__ void map_range(T* o, int64_t e0, int64_t e1, const From& from, F f) {
-    constexpr int V = Elem<T>::kVec;
-    const int off = off_of(o);
-    const int end = (int)((e1 + off + V - 1) / V);
-    for (int base = (int)((e0 + off) / V) + Team<TEAM>::tid(); base < end; base += TEAM * kUnroll) {
-        uint4 r[kUnroll];
-        bool got[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int64_t e = first_of(o, base + u * TEAM);
-            got[u] = e >= e0 && e + V <= e1 && from.get(e, r[u]);
-        }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int64_t e = first_of(o, base + u * TEAM);
-            if (e >= e1) break;
-            float v[V];
-            if (got[u]) {
-                Elem<T>::unpack(r[u], v);
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i) v[i] = e + i >= e0 && e + i < e1 ? from.one(e + i) : neg_inf();
-            }
-            f(v, e);
-            if (e >= e0 && e + V <= e1) {
-                __stcs(reinterpret_cast<uint4*>(o + e), Elem<T>::pack(v));
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (e + i >= e0 && e + i < e1) o[e + i] = Elem<T>::put(v[i]);
-            }
-        }
+// Where a gradient row finds its scores, in vectors of the gradient's alignment: vector j is bytes shift ..
+// shift + 15 of (q[j], q[j + 1]), for lo <= j < hi; element e is p[e].
+template <class T>
+struct Source {
+    const T* p;
+    const uint4* q;
+    int shift, lo, hi;
+    template <bool STREAM>
+    __device__ __forceinline__ uint4 get(int j) const {
+        if (shift) return window(q[j], q[j + 1], shift);  // neighbours read the same bytes: cached
+        return STREAM ? __ldcs(q + j) : q[j];
     }
-}
-
-struct Nothing {
-    __device__ __forceinline__ bool get(int64_t, uint4& v) const {
-        v = make_uint4(0, 0, 0, 0);
-        return true;
-    }
-    __device__ __forceinline__ float one(int64_t) const { return 0.f; }
 };
-template <class T, int TEAM>
-__device__ __forceinline__ void zero_range(T* o, int64_t e0, int64_t e1) {
-    map_range<T, TEAM>(o, e0, e1, Nothing(), [](float* f, int64_t) {
+
+// The scores of a row in memory. Plain loads, not .nc: the gradient may overwrite the scores.
+template <class T>
+__device__ __forceinline__ Source<T> from_row(const T* p, int M, const T* o) {
+    constexpr int V = Elem<T>::kVec;
+    Source<T> s;
+    const int off = off_of(o);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p - off);  // score of the gradient's element -off
+    s.p = p;
+    s.shift = (int)(at & 15u);
+    s.q = reinterpret_cast<const uint4*>(at - s.shift);
+    // the first byte of q[lo] and the last of q[hi - 1 + (shift != 0)] belong to the row
+    const int back = s.shift / (int)sizeof(T);
+    s.lo = (off + back + V - 1) / V;
+    s.hi = (M + off + back) / V - (s.shift ? 1 : 0);
+    return s;
+}
+
+// o[e] = f(score e) for e0 <= e < e1. f(float[V], e) turns the scores of e .. e + V - 1 into gradients. Whole
+// vectors are written as such; what e0, e1 or the source's ends cut is done element by element.
+template <class T, int TEAM, bool STREAM, class F>
+__device__ __forceinline__ void map_range(T* o, int e0, int e1, const Source<T>& from, F f) {
+    constexpr int V = Elem<T>::kVec;
+    const int off = off_of(o), t = Team<TEAM>::tid();
+    const int ja = max((e0 + off + V - 1) / V, from.lo), jb = max(ja, min((e1 + off) / V, from.hi));
+    uint4* out = reinterpret_cast<uint4*>(o - off);
+    int j = ja + t;
+    for (; j + (kUnroll - 1) * TEAM < jb; j += TEAM * kUnroll) {
+        uint4 r[kUnroll];
 #pragma unroll
-        for (int i = 0; i < Elem<T>::kVec; ++i) f[i] = 0.f;
-    });
+        for (int u = 0; u < kUnroll; ++u) r[u] = from.template get<STREAM>(j + u * TEAM);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            float v[V];
+            Elem<T>::unpack(r[u], v);
+            f(v, (j + u * TEAM) * V - off);
+            __stcs(out + j + u * TEAM, Elem<T>::pack(v));
+        }
+    }
+    for (; j < jb; j += TEAM) {
+        float v[V];
+        Elem<T>::unpack(from.template get<STREAM>(j), v);
+        f(v, j * V - off);
+        __stcs(out + j, Elem<T>::pack(v));
+    }
+    const int head = min(e1, ja * V - off), tail = max(head, jb * V - off);
+    const auto one = [&](int e) {
+        float v[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = neg_inf();
+        v[0] = Elem<T>::get(from.p[e]);
+        f(v, e);
+        o[e] = Elem<T>::put(v[0]);
+    };
+    for (int e = e0 + t; e < head; e += TEAM) one(e);
+    for (int e = tail + t; e < e1; e += TEAM) one(e);
+}
+
+template <class T, int TEAM>
+__device__ __forceinline__ void zero_range(T* o, int e0, int e1) {
+    constexpr int V = Elem<T>::kVec;
+    const int off = off_of(o), t = Team<TEAM>::tid();
+    const int ja = (e0 + off + V - 1) / V, jb = max(ja, (e1 + off) / V);
+    for (int j = ja + t; j < jb; j += TEAM) __stcs(reinterpret_cast<uint4*>(o - off) + j, make_uint4(0, 0, 0, 0));
+    const int head = min(e1, ja * V - off), tail = max(head, jb * V - off);
+    for (int e = e0 + t; e < head; e += TEAM) o[e] = Elem<T>::put(0.f);
+    for (int e = tail + t; e < e1; e += TEAM) o[e] = Elem<T>::put(0.f);
 }
 
 // The elements of a part of the row o: whole vectors of it, but at the row's ends.
 struct Range {
-    int64_t e0, e1;
+    int e0, e1;
 };
 template <class T>
 __device__ __forceinline__ Range range_of(const T* o, int M, int rank, int parts) {
     const Slice s = slice_of(vecs_of(o, M), rank, parts);
-    return Range{max(first_of(o, s.begin), (int64_t)0), min(first_of(o, s.end), (int64_t)M)};
+    return Range{max(first_of(o, s.begin), 0), min(first_of(o, s.end), M)};
 }
 
 // The teacher's shares into l.q, by one warp (what distill_row leaves there, in fp32).
@@ -109,19 +136,19 @@ __device__ __forceinline__ void shares(const DistillArgs& a, ListBuf& l) {
 }
 
 // Gradient of the columns from e0 to e1 as if none were listed; w: the row's weight over T.
-template <class T, int TEAM, class From>
-__device__ __forceinline__ void distill_row_grad(const DistillArgs& a, const RowStats& s, float w, T* o, int64_t e0,
-                                                 int64_t e1, const From& from) {
+template <class T, int TEAM, bool STREAM>
+__device__ __forceinline__ void distill_row_grad(const DistillArgs& a, const RowStats& s, float w, T* o, int e0, int e1,
+                                                 const Source<T>& from) {
     const float coef = s.coef * w, gm = s.gm, gls2 = s.gls * kLog2e, c = a.sc.c;
-    map_range<T, TEAM>(o, e0, e1, from, [&](float* f, int64_t) {
+    map_range<T, TEAM, STREAM>(o, e0, e1, from, [&](float* f, int) {
 #pragma unroll
         for (int i = 0; i < Elem<T>::kVec; ++i) f[i] = coef * ex2(fmaf(f[i] - gm, c, -gls2));
     });
 }
 // and of the listed columns from e0 to e1, after a barrier.
 template <class T, int TEAM>
-__device__ __forceinline__ void distill_list_grad(const DistillArgs& a, const RowStats& s, float w, T* o, int64_t e0,
-                                                  int64_t e1, const ListBuf& l, bool twice) {
+__device__ __forceinline__ void distill_list_grad(const DistillArgs& a, const RowStats& s, float w, T* o, int e0,
+                                                  int e1, const ListBuf& l, bool twice) {
     for (int k = Team<TEAM>::tid(); k < a.K; k += TEAM) {
         if (!l.ok(k) || !l.first[k] || l.id[k] < e0 || l.id[k] >= e1) continue;
         float q = l.q[k];

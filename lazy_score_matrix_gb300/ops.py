@@ -358,16 +358,20 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _launch(entry, device, *args):
     """One call of a tp_logits.h entry on the device's current stream."""
-    lib = _lib.load()
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if device.index == torch.cuda.current_device():
-        status = getattr(lib, entry)(*args, stream)
+    call = getattr(_lib.load_logits(), entry)
+    i = device.index
+    if i == torch.cuda.current_device():
+        status = call(*args, _raw_stream(i))
     else:
         with torch.cuda.device(device):
-            status = getattr(lib, entry)(*args, stream)
-    _lib.check(status, entry)
+            status = call(*args, _raw_stream(i))
+    if status != _lib.TP_OK:
+        _lib.check(status, entry)
 
 
 def token_logprobs(logits, tokens, temperature: float = 1.0, top: int = 0, want_stats: bool = False):
