@@ -293,49 +293,39 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     return r;
 }
 
-// N vectors of scores into the state. About nine instructions for two scores: unpack, x - m, the product with c,
-// two ex2, the sums s and h, half a maximum each. A masked score (-inf) makes 0 x inf of its term of h: a sum h
-// that comes out NaN is formed again with the distance bounded, and so are later ones of the thread (`careful`).
-template <class T, int N>
-__device__ __forceinline__ void add_scores(State& st, const uint4 (&r)[N], float c, bool& careful) {
+// N vectors of scores into the state. For two scores: unpacking two, half a maximum each, x - m, the product
+// with c, two ex2 and the sum s. MOMENT: h too; a masked score's distance (-inf) is bounded, as its weight 0 times
+// it would be NaN. Without h, the product is formed with both words of c instead (c_lo > 0, so that -inf stays).
+template <class T, bool MOMENT, int N>
+__device__ __forceinline__ void add_scores(State& st, const uint4 (&r)[N], const Scale& sc) {
     constexpr int V = Elem<T>::kVec;
     const float top = max_nan(Elem<T>::top(r), st.m);
     if (top == neg_inf()) return;
-    st.raise(top, c);
+    st.raise(top, sc.c);
     float2 s[2], h[2];
-    if (!careful) {
-        s[0] = s[1] = h[0] = h[1] = make_float2(0.f, 0.f);
+    s[0] = s[1] = h[0] = h[1] = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int u = 0; u < N; ++u) {
-            float f[V];
-            Elem<T>::unpack(r[u], f);
+    for (int u = 0; u < N; ++u) {
+        float f[V];
+        Elem<T>::unpack(r[u], f);
 #pragma unroll
-            for (int i = 0; i < V; i += 2) {
-                const float2 d = sub2(make_float2(f[i], f[i + 1]), top), x = mul2(d, c);
-                const float2 e = make_float2(ex2(x.x), ex2(x.y));
-                s[i / 2 & 1] = add2(s[i / 2 & 1], e), h[i / 2 & 1] = fma2(e, d, h[i / 2 & 1]);
+        for (int i = 0; i < V; i += 2) {
+            const int k = i / 2 & 1;
+            float2 d = sub2(make_float2(f[i], f[i + 1]), top), x;
+            if (MOMENT) {
+                d = make_float2(max_nan(d.x, -1e30f), max_nan(d.y, -1e30f));
+                x = mul2(d, sc.c);
+            } else {
+                x = fma2(d, make_float2(sc.c_lo, sc.c_lo), mul2(d, sc.c_hi));
             }
-        }
-        h[0] = add2(h[0], h[1]);
-        careful = !(h[0].x + h[0].y <= 0.f);
-    }
-    if (careful) {
-        s[0] = s[1] = h[0] = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int u = 0; u < N; ++u) {
-            float f[V];
-            Elem<T>::unpack(r[u], f);
-#pragma unroll
-            for (int i = 0; i < V; i += 2) {
-                const float2 d = make_float2(max_nan(f[i] - top, -1e30f), max_nan(f[i + 1] - top, -1e30f));
-                const float2 e = make_float2(ex2(d.x * c), ex2(d.y * c));
-                s[i / 2 & 1] = add2(s[i / 2 & 1], e), h[0] = fma2(e, d, h[0]);
-            }
+            const float2 e = make_float2(ex2(x.x), ex2(x.y));
+            s[k] = add2(s[k], e);
+            if (MOMENT) h[k] = fma2(e, d, h[k]);
         }
     }
     const float2 sum = add2(s[0], s[1]);
     st.add(sum.x + sum.y);
-    st.h += h[0].x + h[0].y;
+    if (MOMENT) h[0] = add2(h[0], h[1]), st.h += h[0].x + h[0].y;
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -404,11 +394,6 @@ __device__ __forceinline__ State cluster_merge(const ClusterBuf& b, int size, fl
         all.lo += p.lo, all.h += p.h;
     }
     return all;
-}
-
-// The sum of a state, corrected for the rounding of c (Scale in tp_logits_args.h).
-__device__ __forceinline__ Two exact_sum(const State& st, const Scale& sc) {
-    return two_sum(st.s, st.lo + sc.delta * st.h);
 }
 
 // r with the elements whose bits are set masked (few vectors have any)
@@ -559,7 +544,6 @@ __device__ __forceinline__ State read_slice(const DistillArgs& a, const RowVecs<
     constexpr int V = Elem<T>::kVec, kMarkVecs = Marks<TEAM>::kCols / V;
     const int t = Team<TEAM>::tid();
     State st;
-    bool careful = false;
     for (int part = sl.begin; part < sl.end; part += REST ? kMarkVecs : sl.end) {
         const int end = REST ? min(sl.end, part + kMarkVecs) : sl.end;
         uint4 next[kUnroll];  // a chunk is under way while the one before it is reduced
@@ -577,7 +561,7 @@ __device__ __forceinline__ State read_slice(const DistillArgs& a, const RowVecs<
                     r[u] = without<T>(r[u], marks.bits[bit >> 5] >> (bit & 31));
                 }
             }
-            add_scores<T>(st, r, a.sc.c, careful);
+            add_scores<T, false>(st, r, a.sc);
         }
     }
     return st;
@@ -595,7 +579,7 @@ struct RowStats {
 // or of the unlisted ones (rest).
 __device__ __forceinline__ RowStats close_row(const DistillArgs& a, const State& st, const ListBuf& b) {
     const ListSums& l = b.sums;
-    const Two zs = exact_sum(st, a.sc);
+    const Two zs = two_sum(st.s, st.lo);
     float m = st.m;  // maximum over all columns
     Two z = zs;      // sum over all columns, relative to m
     if (a.rest && l.zl.h > 0.f) {

@@ -122,7 +122,10 @@ Scale scale_of(double t) {
     const double inv = 1.0 / t;
     s.inv = (float)inv;
     s.inv_lo = (float)(inv - (double)s.inv);
-    s.c = (float)(1.4426950408889634074 / t);
+    const double c = 1.4426950408889634074 / t;
+    s.c = (float)c;
+    s.c_hi = std::nextafterf((float)c, 0.f);  // below c whichever way it rounded
+    s.c_lo = (float)(c - (double)s.c_hi);
     s.delta = (float)(inv - (double)s.c * 0.69314718055994530942);
     return s;
 }

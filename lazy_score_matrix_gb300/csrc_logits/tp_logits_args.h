@@ -23,11 +23,13 @@ struct View {
     int M, group;
 };
 
-// The temperature as the kernels use it: c = log2(e)/T rounded to fp32 (exponents are 2^(c d)), inv = 1/T, and
-// delta = 1/T - c ln 2, what the rounding of c takes from the exponent's slope: a sum s of exponentials
-// with first moment h is corrected to s + delta h.
+// The temperature as the kernels use it. c = log2(e)/T rounded to fp32 (exponents are 2^(c d)); its rounding is a
+// slightly other temperature for the whole row, which a loss near zero shows. Two ways out: delta = 1/T - c ln 2
+// corrects a sum s of exponentials with first moment h to s + delta h; or exponents are formed with c_hi + c_lo =
+// log2(e)/T, c_lo > 0.
 struct Scale {
-    float c, delta, inv, inv_lo;  // inv + inv_lo = 1/T
+    float c, delta, c_hi, c_lo;
+    float inv, inv_lo;  // inv + inv_lo = 1/T
 };
 
 struct LogprobArgs {

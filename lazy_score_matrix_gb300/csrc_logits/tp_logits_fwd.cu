@@ -170,7 +170,6 @@ __global__ void __launch_bounds__(kThreads, TOP && TEAM != 32 ? 6 : 4) logprobs_
     Tops<TEAM> best(tops[TOP ? Tm::id() : 0], a.top);
     if (TOP) best.clear();
     State st;
-    bool careful = false;
     uint4 next[kUnroll];  // without alternatives, a chunk is under way while the one before it is reduced
     if (!TOP) x.load(next, sl.begin + t, TEAM, sl.end);
     for (int base = sl.begin; base < sl.end; base += TEAM * kUnroll) {
@@ -182,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, TOP && TEAM != 32 ? 6 : 4) logprobs_
             for (int u = 0; u < kUnroll; ++u) r[u] = next[u];
             x.load(next, base + TEAM * kUnroll + t, TEAM, sl.end);
         }
-        add_scores<T>(st, r, a.sc.c, careful);
+        add_scores<T, true>(st, r, a.sc);
         if (TOP) {
             if (base == sl.begin) best.start(st.m, sizeof(T) == 2 ? 1ull << 44 : 1ull << 32);
             const float bar = best.bar(x.first(base));

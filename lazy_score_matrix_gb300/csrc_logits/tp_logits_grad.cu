@@ -101,7 +101,6 @@ __global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillArg
     }
         if (TEAM == 32 || threadIdx.x < 32) sum_list(a, list);
     State st;
-    bool careful = false;
     int left = (n - t + TEAM * kUnroll - 1) / (TEAM * kUnroll);  // groups of this thread
     for (int i = t; i < n; i += TEAM * kUnroll) {
         copies_wait(--left);
@@ -112,7 +111,7 @@ __global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillArg
             r[u] = j < n ? buf[j] : Elem<T>::none();
             if (REST && j < n) r[u] = without<T>(r[u], marks[j * V >> 5] >> (j * V & 31));
         }
-        add_scores<T>(st, r, a.sc.c, careful);
+        add_scores<T, false>(st, r, a.sc);
     }
     st = team_state<TEAM>(st, a.sc.c, red);
     if (size > 1) {
