@@ -19,12 +19,14 @@
 namespace tp {
 namespace rows {
 
-constexpr int kThreads = 256;  // per CTA, but of the kernel for long rows
+constexpr int kThreads = 256;      // per CTA
+constexpr int kLongThreads = 512;  // where a row is read twice: fewer rows under way, for the second reading to hit the cache
 constexpr int kUnroll = 4;     // 16-byte vectors a thread has in flight
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718f;
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+__device__ __forceinline__ float lowest() { return __uint_as_float(0xff7fffffu); }
 __device__ __forceinline__ float ex2(float x) { return ExpTraits<float>::bexp(x); }
 // maximum that keeps a NaN of either operand, so that a NaN score reaches the row's results
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -40,6 +42,11 @@ struct Elem<float> {
     static constexpr int kVec = 4;  // elements of a 16-byte vector
     __device__ __forceinline__ static float get(float v) { return v; }
     __device__ __forceinline__ static float put(float v) { return v; }
+    // whether an element of r reaches a bar
+    __device__ __forceinline__ static float bar(float v) { return v; }
+    __device__ __forceinline__ static bool reaches(const uint4& r, float b) {
+        return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w))) >= b;
+    }
     __device__ __forceinline__ static uint4 none() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
     template <int N>
     __device__ __forceinline__ static float top(const uint4 (&r)[N]) {
@@ -71,6 +78,11 @@ struct Elem<__half> {
             m = __hmax2_nan(__hmax2_nan(m, __hmax2_nan(of(r[u].x), of(r[u].y))), __hmax2_nan(of(r[u].z), of(r[u].w)));
         return max_nan(__half2float(__low2half(m)), __half2float(__high2half(m)));
     }
+    // the smallest value of the type that reaches v, twice
+    __device__ __forceinline__ static __half2 bar(float v) { return __half2half2(__float2half_ru(v)); }
+    __device__ __forceinline__ static bool reaches(const uint4& r, __half2 b) {
+        return (__hge2_mask(of(r.x), b) | __hge2_mask(of(r.y), b) | __hge2_mask(of(r.z), b) | __hge2_mask(of(r.w), b)) != 0;
+    }
     __device__ __forceinline__ static __half2 of(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
     __device__ __forceinline__ static __half put(float v) { return __float2half_rn(v); }
     __device__ __forceinline__ static uint32_t two(float a, float b) {
@@ -101,6 +113,11 @@ struct Elem<__nv_bfloat16> {
         for (int u = 0; u < N; ++u)
             m = __hmax2_nan(__hmax2_nan(m, __hmax2_nan(of(r[u].x), of(r[u].y))), __hmax2_nan(of(r[u].z), of(r[u].w)));
         return max_nan(__bfloat162float(__low2bfloat16(m)), __bfloat162float(__high2bfloat16(m)));
+    }
+    // the smallest value of the type that reaches v, twice
+    __device__ __forceinline__ static __nv_bfloat162 bar(float v) { return __bfloat162bfloat162(__float2bfloat16_ru(v)); }
+    __device__ __forceinline__ static bool reaches(const uint4& r, __nv_bfloat162 b) {
+        return (__hge2_mask(of(r.x), b) | __hge2_mask(of(r.y), b) | __hge2_mask(of(r.z), b) | __hge2_mask(of(r.w), b)) != 0;
     }
     __device__ __forceinline__ static __nv_bfloat162 of(uint32_t u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); }
     __device__ __forceinline__ static __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
@@ -348,8 +365,8 @@ struct ReduceBuf {
     float m[32], s[32], lo[32], h[32];
 };
 
-// The state of all scores of the team, in every thread. A CTA's takes two barriers; the buffer may be used
-// again after the caller's next one.
+// The state of all scores of the team, in every thread of its first warp; the others have its maximum. A CTA's
+// takes two barriers; the buffer may be used again after the caller's next one.
 template <int TEAM>
 __device__ __forceinline__ State team_state(State st, float c, ReduceBuf& b) {
     constexpr int W = TEAM / 32;
@@ -367,6 +384,7 @@ __device__ __forceinline__ State team_state(State st, float c, ReduceBuf& b) {
     warp_sum(st);
     if (lane == 0) b.s[w] = st.s, b.lo[w] = st.lo, b.h[w] = st.h;
     __syncthreads();
+    if (w != 0) return st;
     st.s = lane < W ? b.s[lane] : 0.f, st.lo = lane < W ? b.lo[lane] : 0.f, st.h = lane < W ? b.h[lane] : 0.f;
     warp_sum(st);
     return st;
@@ -376,7 +394,8 @@ constexpr int kMaxCluster = 8;
 struct ClusterBuf {
     float4 part[kMaxCluster];
 };
-// Every CTA's state to every CTA of the cluster; the caller then crosses a cluster barrier and merges.
+// Every CTA's state to every CTA of the cluster (by its first warp); the caller then crosses a cluster barrier and
+// merges.
 __device__ __forceinline__ void cluster_share(const State& st, ClusterBuf& b, int rank, int size) {
     if ((int)threadIdx.x < size) of_rank(&b, threadIdx.x)->part[rank] = make_float4(st.m, st.s, st.lo, st.h);
 }

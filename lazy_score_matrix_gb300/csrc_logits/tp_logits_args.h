@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "tp_logits.h"
 
 namespace tp {
@@ -80,6 +82,25 @@ inline Shape shape_of(int64_t N, int64_t M, bool warps, int64_t chunk) {
     s.grid = (unsigned)(s.warp ? (N + 7) / 8 : N * s.cluster);
     return s;
 }
+
+// Lets a kernel use so many bytes of dynamic shared memory; `ready` remembers the devices where it may, bit by bit.
+// An error is left for the launch check.
+template <class K>
+inline bool raise_smem(K kernel, size_t bytes, std::atomic<uint64_t>& ready) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (ready.load(std::memory_order_relaxed) & bit) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
+
+// Kernels that read a row twice want it in the L2 cache (129 MB) the second time: the rows under way on the whole
+// card may take so much of it. Where the CTAs that an SM's registers admit would have more, one is kept alone
+// on its SM by shared memory that it does not use.
+constexpr int64_t kCacheBytes = (int64_t)110 << 20;
+constexpr size_t kAlone = 120 * 1024;
 
 template <class... KArgs, class... Args>
 inline void launch(void (*kernel)(KArgs...), const Shape& sh, cudaStream_t s, const Args&... a) {

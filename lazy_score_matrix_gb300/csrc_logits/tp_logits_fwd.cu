@@ -2,6 +2,8 @@
 // softmax state in registers; the alternatives are filtered in the same pass.
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "tp_launch.h"
 #include "tp_logits.cuh"
 
@@ -9,14 +11,16 @@ namespace tp {
 namespace rows {
 namespace {
 
-// Alternatives. Candidates (keys) collect in shared memory; keys at or below `thr` cannot be among the best
-// `top` and are dropped. When the buffer is full it is cut back to at most kSlack keys more than `top`.
-constexpr int kSlack = 16;
+// Alternatives. When a row has been read once, the top-th largest of its threads' own maxima bounds the top-th
+// largest score from below: that many threads hold a column that reaches it. A second reading of the row, from
+// the cache, collects the columns that reach the bound; of 128K columns under 512 threads that is about 1.2 times
+// `top`. They are ranked by counting, each against all others. Where ties let more columns through than the
+// buffer holds, it is cut back to the best ones by bisection and the bound becomes a key (value and column).
 template <int TEAM>
 struct TopBuf {
-    static constexpr int kCap = TEAM == 32 ? 256 : kMaxCluster * (kMaxList + kSlack);
+    static constexpr int kCap = TEAM == 32 ? 256 : 2048, kKeep = TEAM == 32 ? 96 : kCap / kMaxCluster;
     unsigned long long key[kCap];
-    unsigned long long thr;
+    unsigned long long thr;  // keys at or below it cannot be among the best
     int cnt;
     uint32_t slot[3];  // reductions of a CTA, in turn: one in use, one read, one cleared
 };
@@ -24,7 +28,7 @@ struct TopBuf {
 template <int TEAM>
 struct Tops {
     using Buf = TopBuf<TEAM>;
-    static constexpr int kPer = (Buf::kCap + TEAM - 1) / TEAM;  // keys a thread looks at
+    static constexpr int kPer = Buf::kCap / TEAM;  // keys a thread looks at
     Buf& b;
     const int top;
     int turn = 0;
@@ -53,35 +57,44 @@ struct Tops {
         return reduce(v, [](uint32_t* s, uint32_t x) { atomicMax(s, x); }, [](uint32_t x) { return __reduce_max_sync(~0u, x); });
     }
 
-    // A key that at least k of the team's cnt keys (all above `above`) reach, by bisection, until at most `limit`
-    // do or the bounds are `grain` apart. `key` are the thread's own of them (0: none).
-    __device__ __forceinline__ unsigned long long bound(const unsigned long long (&key)[kPer], int cnt, int k, int limit,
-                                                        unsigned long long above, unsigned long long grain) {
+    // The bound from every thread's largest score (-inf: none): an order (ord_of) that at least `top` of them reach,
+    // or 0. `grain`: the step of the scores' type in it.
+    __device__ __forceinline__ uint32_t bound(float best, uint32_t grain) {
+        const uint32_t o = best > neg_inf() ? ord_of(best) : 0;
+        int n = Team<TEAM>::count(o != 0);
+        if (n < top) return 0;
+        uint32_t lo = ~max(o ? ~o : 0), hi = max(o) + 1;  // smallest and largest
+        while (n > top + top / 8 && hi - lo > grain) {
+            const uint32_t mid = lo + (hi - lo) / 2;
+            const int c = Team<TEAM>::count(o >= mid);
+            if (c >= top) lo = mid, n = c;
+            else hi = mid;
+        }
+        return lo;
+    }
+    // Cuts the buffer back to at most kKeep keys, the best `top` among them. Barriers on both sides.
+    __device__ __noinline__ void cut() {
+        Team<TEAM>::sync();
+        const int t = Team<TEAM>::tid();
+        int n = min(b.cnt, Buf::kCap);
+        if (n <= Buf::kKeep) return;
+        unsigned long long key[kPer];
         uint32_t m = 0;
 #pragma unroll
-        for (int r = 0; r < kPer; ++r) m = ::max(m, (uint32_t)(key[r] >> 32));
-        unsigned long long lo = above + 1, hi = ((unsigned long long)max(m) + 1) << 32;
-        int n = cnt;
-        while (n > limit && hi - lo > grain) {
+        for (int r = 0; r < kPer; ++r) {
+            key[r] = t + r * TEAM < n ? b.key[t + r * TEAM] : 0;
+            m = ::max(m, (uint32_t)(key[r] >> 32));
+        }
+        unsigned long long lo = b.thr + 1, hi = ((unsigned long long)max(m) + 1) << 32;
+        while (n > Buf::kKeep) {  // keys differ: this ends at the latest when lo and hi are neighbours
             const unsigned long long mid = lo + (hi - lo) / 2;
             uint32_t c = 0;
 #pragma unroll
             for (int r = 0; r < kPer; ++r) c += key[r] >= mid;
             c = sum(c);
-            if ((int)c >= k) lo = mid, n = (int)c;
+            if ((int)c >= top) lo = mid, n = (int)c;
             else hi = mid;
         }
-        return lo;
-    }
-    // Cuts the buffer back to at most top + kSlack keys, the best `top` among them. Barriers on both sides.
-    __device__ __forceinline__ void cut() {
-        Team<TEAM>::sync();
-        const int t = Team<TEAM>::tid(), cnt = min(b.cnt, Buf::kCap);
-        if (cnt <= top + kSlack) return;
-        unsigned long long key[kPer];
-#pragma unroll
-        for (int r = 0; r < kPer; ++r) key[r] = t + r * TEAM < cnt ? b.key[t + r * TEAM] : 0;
-        const unsigned long long lo = bound(key, cnt, top, top + kSlack, b.thr, 1);
         Team<TEAM>::sync();
         if (t == 0) b.cnt = 0, b.thr = lo - 1;
         Team<TEAM>::sync();
@@ -90,36 +103,54 @@ struct Tops {
             if (key[r] >= lo) b.key[atomicAdd(&b.cnt, 1)] = key[r];
         Team<TEAM>::sync();
     }
-    // A first threshold, from every thread's best value so far: `top` threads that reach it are as many columns.
-    // `grain`: the step of the scores' type in a key (fp16 and bf16 leave the low bits of an fp32 value alone).
-    __device__ __forceinline__ void start(float best, unsigned long long grain) {
-        unsigned long long key[kPer];
-#pragma unroll
-        for (int r = 0; r < kPer; ++r) key[r] = 0;
-        if (best > neg_inf()) key[0] = (unsigned long long)ord_of(best) << 32;
-        const int have = (int)sum(key[0] != 0);
-        if (have < top) return;
-        const unsigned long long lo = bound(key, have, top, top + top / 8, 0, grain);
-        if (Team<TEAM>::tid() == 0) b.thr = lo - 1;
-        Team<TEAM>::sync();
-    }
     // The value that a column from `col` on has to reach. A key at the threshold's value but of a later column
     // is below the threshold, so the bar is then one step higher.
-    __device__ __forceinline__ float bar(int64_t col) const {
+    __device__ __forceinline__ float bar(int col) const {
         const unsigned long long thr = b.thr;
-        if (thr == 0) return __uint_as_float(0xff7fffffu);  // anything above -inf
-        const uint32_t o = ::max((uint32_t)(thr >> 32), 0x00800000u);  // a bound may lie below every finite value
-        return of_ord((int64_t)(uint32_t)~(uint32_t)thr < col ? o + 1 : o);
+        if (thr == 0) return lowest();
+        const uint32_t o = ::max((uint32_t)(thr >> 32), ord_of(lowest()));  // a bound may lie below every finite value
+        return of_ord(~(uint32_t)thr < (uint32_t)col ? o + 1 : o);
     }
-    // Offer this thread's elements of a chunk: bit i of `mask` stands for column col(i), value val(i).
-    template <class Col, class Val>
-    __device__ __forceinline__ void offer(uint32_t mask, Col col, Val val) {
+    // The columns of this thread's vectors (vector u at column col0 + u step) that reach the bar, to the buffer as
+    // long as it has room; cnt counts them all.
+    template <class T, int N>
+    __device__ __forceinline__ void collect(const uint4 (&r)[N], int col0, int step, float bar) {
+        constexpr int V = Elem<T>::kVec;
+        const auto type_bar = Elem<T>::bar(bar);
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+            if (Elem<T>::reaches(r[u], type_bar)) {  // few do
+                float f[V];
+                Elem<T>::unpack(r[u], f);
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (f[i] >= bar) {
+                        const int at = atomicAdd(&b.cnt, 1);
+                        if (at < Buf::kCap) b.key[at] = key_of(f[i], col0 + u * step + i);
+                    }
+            }
+    }
+    // The same for a row of more of them than the buffer holds: the whole team calls it, and cuts the buffer back
+    // whenever it is full.
+    template <class T, int N>
+    __device__ __forceinline__ void offer(const uint4 (&r)[N], const T* p, int col0, int step, float bar) {
+        constexpr int V = Elem<T>::kVec;
+        const auto top_bar = Elem<T>::bar(bar);
+        uint32_t mask = 0;
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+            if (Elem<T>::reaches(r[u], top_bar)) {  // few do
+                float f[V];
+                Elem<T>::unpack(r[u], f);
+#pragma unroll
+                for (int i = 0; i < V; ++i) mask |= f[i] >= bar ? 1u << (u * V + i) : 0u;
+            }
         while (true) {
-            uint32_t left = 0;
             const unsigned long long thr = b.thr;
-            for (uint32_t m = mask; m; m &= m - 1) {
-                const int i = __ffs(m) - 1;
-                const unsigned long long k = key_of(val(i), col(i));
+            uint32_t left = 0;  // what finds no room
+            for (; mask; mask &= mask - 1) {
+                const int i = __ffs(mask) - 1, col = col0 + i / V * step + i % V;
+                const unsigned long long k = key_of(Elem<T>::get(p[col]), col);
                 if (k <= thr) continue;
                 const int at = atomicAdd(&b.cnt, 1);
                 if (at < Buf::kCap) b.key[at] = k;
@@ -142,19 +173,21 @@ __device__ __forceinline__ void leave_out(const LogprobArgs& a, int64_t row, int
     for (int i = t; i < a.top; i += team) a.top_logprobs[row * a.top + i] = neg_inf(), a.top_ids[row * a.top + i] = -1;
 }
 
-struct Gather {  // the candidates of a cluster's other CTAs
-    unsigned long long key[kMaxCluster][kMaxList + kSlack];
+struct Gather {  // the candidates of a cluster's CTAs, in the first of them
+    static constexpr int kMost = TopBuf<kThreads>::kKeep;
+    unsigned long long key[kMaxCluster][kMost];
     int n[kMaxCluster];
 };
 
 template <class T, int TEAM, bool TOP>
-__global__ void __launch_bounds__(kThreads, TOP && TEAM != 32 ? 6 : 4) logprobs_kernel(const LogprobArgs a) {
+__global__ void __launch_bounds__(TEAM == 32 ? kThreads : TEAM, TEAM == kLongThreads ? 2 : 4) logprobs_kernel(const LogprobArgs a) {
     constexpr int V = Elem<T>::kVec;
     using Tm = Team<TEAM>;
     __shared__ ReduceBuf red;
     __shared__ ClusterBuf parts;
     __shared__ TopBuf<TEAM> tops[TOP ? Tm::kPerCta : 1];
     __shared__ Gather others[1];
+    __shared__ uint32_t bounds[kMaxCluster];
     const int rank = TEAM == 32 ? 0 : cluster_rank(), size = TEAM == 32 ? 1 : cluster_size();
     const int64_t row = TEAM == 32 ? (int64_t)blockIdx.x * Tm::kPerCta + Tm::id() : blockIdx.x / size;
     if (row >= a.N) return;
@@ -167,65 +200,80 @@ __global__ void __launch_bounds__(kThreads, TOP && TEAM != 32 ? 6 : 4) logprobs_
     if (size > 1) cluster_arrive();
     const RowVecs<T> x(row_at<const T>(a.x, row), a.x.M);
     const Slice sl = slice_of(x.n, rank, size);
-    Tops<TEAM> best(tops[TOP ? Tm::id() : 0], a.top);
-    if (TOP) best.clear();
     State st;
-    uint4 next[kUnroll];  // without alternatives, a chunk is under way while the one before it is reduced
-    if (!TOP) x.load(next, sl.begin + t, TEAM, sl.end);
+    uint4 next[kUnroll];  // a chunk is under way while the one before it is reduced
+    x.load(next, sl.begin + t, TEAM, sl.end);
     for (int base = sl.begin; base < sl.end; base += TEAM * kUnroll) {
         uint4 r[kUnroll];
-        if (TOP) {
-            x.load(r, base + t, TEAM, sl.end);
-        } else {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) r[u] = next[u];
+        x.load(next, base + TEAM * kUnroll + t, TEAM, sl.end);
+        add_scores<T, true>(st, r, a.sc);
+    }
+    const float own = st.m;
+    st = team_state<TEAM>(st, a.sc.c, red);
+    Tops<TEAM> best(tops[TOP ? Tm::id() : 0], a.top);
+    uint32_t bound = 0;
+    if (TOP) {
+        best.clear();
+        bound = best.bound(own, sizeof(T) == 2 ? 1u << 12 : 1u);
+    }
+    if (size > 1) {
+        cluster_wait();  // every CTA of the cluster runs
+        cluster_share(st, parts, rank, size);
+        if (TOP && t < size) of_rank(bounds, t)[rank] = bound;
+        cluster_arrive();
+        cluster_wait();
+        if (!TOP && rank != 0) return;
+        st = cluster_merge(parts, size, a.sc.c);
+        if (TOP)
+            for (int r = 0; r < size; ++r) bound = max(bound, bounds[r]);  // each holds for the whole row
+    }
+    if (TOP) {
+        const float bar = bound ? of_ord(bound) : lowest();
+        x.load(next, sl.begin + t, TEAM, sl.end);
+        for (int base = sl.begin; base < sl.end; base += TEAM * kUnroll) {
+            uint4 r[kUnroll];
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) r[u] = next[u];
             x.load(next, base + TEAM * kUnroll + t, TEAM, sl.end);
+            best.template collect<T>(r, x.first(base + t), TEAM * V, bar);
         }
-        add_scores<T, true>(st, r, a.sc);
-        if (TOP) {
-            if (base == sl.begin) best.start(st.m, sizeof(T) == 2 ? 1ull << 44 : 1ull << 32);
-            const float bar = best.bar(x.first(base));
-            uint32_t mask = 0;
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                float f[V];
-                Elem<T>::unpack(r[u], f);
-#pragma unroll
-                for (int i = 0; i < V; ++i) mask |= f[i] >= bar ? 1u << (u * V + i) : 0u;
+        Tm::sync();
+        if (best.b.cnt > TopBuf<TEAM>::kCap) {
+            Tm::sync();
+            if (t == 0) best.b.cnt = 0, best.b.thr = bound ? ((unsigned long long)bound << 32) - 1 : 0;
+            Tm::sync();
+            for (int base = sl.begin; base < sl.end; base += TEAM * kUnroll) {
+                uint4 r[kUnroll];
+                x.load(r, base + t, TEAM, sl.end);
+                best.template offer<T>(r, x.p, x.first(base + t), TEAM * V, best.bar(max(x.first(base), 0)));
             }
-            const auto col = [&](int i) { return x.first(base + (i / V) * TEAM + t) + i % V; };
-            best.offer(mask, col, [&](int i) { return Elem<T>::get(x.p[col(i)]); });
         }
-    }
-    st = team_state<TEAM>(st, a.sc.c, red);
-    if (size > 1) {
-        if (TOP) best.cut();
-        cluster_wait();  // every CTA of the cluster runs
-        cluster_share(st, parts, rank, size);
-        if (TOP) {
+        if (size > 1) {
+            best.cut();
             Gather* g = of_rank(&others[0], 0);
-            const int n = min(best.b.cnt, a.top + kSlack);
+            const int n = best.b.cnt;
             for (int i = t; i < n; i += TEAM) g->key[rank][i] = best.b.key[i];
             if (t == 0) g->n[rank] = n;
-        }
-        cluster_arrive();
-        cluster_wait();
-        if (rank != 0) return;
-        st = cluster_merge(parts, size, a.sc.c);
-        if (TOP) {
+            cluster_arrive();
+            cluster_wait();
+            if (rank != 0) return;
             int at = 0;
             for (int r = 0; r < size; ++r) {
-                const int n = others[0].n[r];
-                for (int i = t; i < n; i += TEAM) best.b.key[at + i] = others[0].key[r][i];
-                at += n;
+                const int m = others[0].n[r];
+                for (int i = t; i < m; i += TEAM) best.b.key[at + i] = others[0].key[r][i];
+                at += m;
             }
+            Tm::sync();
             if (t == 0) best.b.cnt = at, best.b.thr = 0;
         }
     }
     const bool some = st.m != neg_inf();
     const float z = st.s + (st.lo + a.sc.delta * st.h);
-    const float ls = some ? logf(z) : 0.f;
+    float ls = some ? logf(z) : 0.f;
     if (t == 0) {
+        if (TOP) red.s[0] = ls;  // to the other warps
         const float H = some ? ls - st.h / z * a.sc.inv : 0.f;
         a.entropy[row] = H;
         if (a.logprobs) a.logprobs[row] = some ? (Elem<T>::get(x.p[tok]) - st.m) * a.sc.inv - ls : neg_inf();
@@ -237,7 +285,8 @@ __global__ void __launch_bounds__(kThreads, TOP && TEAM != 32 ? 6 : 4) logprobs_
     }
     if (TOP) {
         best.cut();
-        const int n = min(best.b.cnt, a.top + kSlack);
+        if (TEAM != 32) ls = red.s[0];
+        const int n = best.b.cnt;
         for (int i = t; i < n; i += TEAM) {  // the keys differ: a key's place is the number of larger ones
             const unsigned long long k = best.b.key[i];
             int place = 0;
@@ -306,13 +355,22 @@ constexpr int64_t kChunk = kThreads * kUnroll * Elem<T>::kVec;
 template <class T>
 void run_logprobs(const LogprobArgs& a, cudaStream_t s) {
     HookScope h("token_logprobs", s);
-    const Shape sh = shape_of(a.N, a.x.M, a.top <= 32, kChunk<T>);
+    Shape sh = shape_of(a.N, a.x.M, a.top <= 32, kChunk<T>);
+    const int64_t row = (int64_t)a.x.M * (int64_t)sizeof(T);
     if (sh.warp) {
         if (a.top) launch(logprobs_kernel<T, 32, true>, sh, s, a);
         else launch(logprobs_kernel<T, 32, false>, sh, s, a);
+    } else if (a.top && sh.cluster == 1 && 4 * kSms * row <= kCacheBytes) {
+        launch(logprobs_kernel<T, kThreads, true>, sh, s, a);
+    } else if (a.top) {
+        auto kernel = logprobs_kernel<T, kLongThreads, true>;
+        static std::atomic<uint64_t> ready{0};
+        sh.threads = kLongThreads;
+        if (sh.cluster == 1 && a.N > kSms && 2 * kSms * row > kCacheBytes) sh.smem = kAlone;
+        if (sh.smem && !raise_smem(kernel, kAlone, ready)) return;
+        launch(kernel, sh, s, a);
     } else {
-        if (a.top) launch(logprobs_kernel<T, kThreads, true>, sh, s, a);
-        else launch(logprobs_kernel<T, kThreads, false>, sh, s, a);
+        launch(logprobs_kernel<T, kThreads, false>, sh, s, a);
     }
 }
 template <class T>

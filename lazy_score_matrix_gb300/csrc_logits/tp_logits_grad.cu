@@ -151,22 +151,8 @@ constexpr size_t kSmemThree = 68 * 1024;     // three CTAs an SM
 constexpr int64_t kManyRows = 2 * kSms;
 constexpr int64_t kWarpBytes = 4096;         // rows up to this long: one warp a row
 
-// Lets a kernel use so many bytes of dynamic shared memory; `ready` remembers the devices where it may, bit by
-// bit. An error is left for the launch check.
-template <class K>
-bool raise_smem(K kernel, size_t bytes, std::atomic<uint64_t>& ready) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-    if (ready.load(std::memory_order_relaxed) & bit) return true;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
-    ready.fetch_or(bit, std::memory_order_relaxed);
-    return true;
-}
-
 // Rows too long for that, or for enough of them on an SM: one CTA a row reads it twice, and the second time it comes
 // from the L2 cache, as long as the rows under way on the whole card fit there (go_long).
-constexpr int kLongThreads = 512;
 
 template <class T, bool REST>
 __global__ void __launch_bounds__(kLongThreads, 2) distill_grad_long_kernel(const DistillArgs a) {
@@ -210,8 +196,6 @@ __global__ void __launch_bounds__(kLongThreads, 2) distill_grad_long_kernel(cons
     distill_list_grad<T, TEAM>(a, s, w, o, 0, M, list, twice);
 }
 
-constexpr int64_t kCacheBytes = (int64_t)110 << 20;  // of rows under way, to be found in L2 again
-constexpr size_t kAlone = 120 * 1024;  // dynamic shared memory of which two do not fit an SM
 template <class T, bool REST>
 void go_long(const DistillArgs& a, cudaStream_t s) {
     auto kernel = distill_grad_long_kernel<T, REST>;
