@@ -43,7 +43,7 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     Differentiable in logprobs and entropy; the alternatives carry no gradient. temperature in [1e-3, 1e3]."""
     if torch.is_grad_enabled() and isinstance(logits, torch.Tensor) and logits.requires_grad:
         return TokenLogprobs(*_TokenLogprobsFn.apply(logits, tokens, float(temperature), int(top)))
-    return TokenLogprobs(*ops.token_logprobs(logits, tokens, temperature, top)[:4])
+    return TokenLogprobs(*ops.token_logprobs(logits, tokens, float(temperature), int(top))[:4])
 
 
 def topk_distillation(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_values: torch.Tensor, *,
@@ -66,7 +66,7 @@ def topk_distillation(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_v
         raise ValueError("topk_distillation: the teacher's list is a constant; pass teacher_values.detach()")
     if torch.is_grad_enabled() and isinstance(logits, torch.Tensor) and logits.requires_grad:
         return _TopkDistillationFn.apply(logits, teacher_ids, teacher_values, float(temperature), bool(rest))
-    return ops.topk_distillation(logits, teacher_ids, teacher_values, temperature, rest)[0]
+    return ops.topk_distillation(logits, teacher_ids, teacher_values, float(temperature), rest)[0]
 
 
 @torch.no_grad()
@@ -78,19 +78,30 @@ def topk_distillation_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teac
     read once for both, so this is the form for training: ``logits.backward(gradient)``.
 
     out: where the gradient is written; it may be the logits themselves, which are then overwritten."""
-    loss, grad = ops.topk_distillation_grad(logits, teacher_ids, teacher_values, weights, temperature, rest, out)
+    loss, grad = ops.topk_distillation_grad(logits, teacher_ids, teacher_values, weights, float(temperature), rest, out)
     if out is not None:
         torch.autograd.graph.increment_version(out)  # a graph that saved it must not use it any more
     return loss, grad
 
 
+# The forwards keep what their backwards need in the form that the C entry takes: a backward runs on autograd's own
+# thread, where every step costs twice what it does on the caller's.
+
+
+def _dense(g):
+    return g if g is None or g.is_contiguous() else g.contiguous()
+
+
 class _TokenLogprobsFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, tokens, temperature, top):
-        lp, h, topv, topi, stats = ops.token_logprobs(logits, tokens, temperature, top, want_stats=True)
+        ctx.rows, kept = ops._rows(logits)
+        tokens = ops._side(tokens, torch.int64, "tokens", logits.shape[:-1], logits)
+        lp, h, topv, topi, stats = ops.token_logprobs(kept, tokens, temperature, top, want_stats=True)
         ctx.set_materialize_grads(False)
-        ctx.mark_non_differentiable(*[t for t in (topv, topi) if t is not None])
-        ctx.save_for_backward(logits, tokens, stats)
+        if top:
+            ctx.mark_non_differentiable(topv, topi)
+        ctx.save_for_backward(kept, tokens, stats)
         ctx.temperature = temperature
         return lp, h, topv, topi
 
@@ -100,14 +111,16 @@ class _TokenLogprobsFn(torch.autograd.Function):
         if g_lp is None and g_h is None:
             return None, None, None, None
         logits, tokens, stats = ctx.saved_tensors
-        return ops.token_logprobs_backward(logits, tokens, ctx.temperature, stats, g_lp, g_h), None, None, None
+        return ops._logprobs_grad(logits, ctx.rows, tokens, ctx.temperature, stats, _dense(g_lp), _dense(g_h)), None, None, None
 
 
 class _TopkDistillationFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, ids, values, temperature, rest):
-        loss, stats = ops.topk_distillation(logits, ids, values, temperature, rest, want_stats=True)
-        ctx.save_for_backward(logits, ids, values, stats)
+        ctx.rows, kept = ops._rows(logits)
+        _, ids, values = ops._teacher(kept, ctx.rows, ids, values)
+        loss, stats = ops.topk_distillation(kept, ids, values, temperature, rest, want_stats=True)
+        ctx.save_for_backward(kept, ids, values, stats)
         ctx.temperature, ctx.rest = temperature, rest
         return loss
 
@@ -115,4 +128,5 @@ class _TopkDistillationFn(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, gl):
         logits, ids, values, stats = ctx.saved_tensors
-        return ops.topk_distillation_backward(logits, ids, values, ctx.temperature, ctx.rest, stats, gl), None, None, None, None
+        return (ops._distillation_grad(logits, ctx.rows, ids, values, ctx.temperature, ctx.rest, stats, _dense(gl)),
+                None, None, None, None)

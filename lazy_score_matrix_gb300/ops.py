@@ -317,23 +317,26 @@ def _row_strides(t):
 
 def _rows(t, name="logits", copy=True):
     """The tp_rows of t [..., M] and the tensor it points into (a contiguous copy where its strides need one)."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in _ROWS_DT:
+    kind = _ROWS_DT.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if kind is None:
         raise TypeError(f"{name} must be a float32, float16 or bfloat16 tensor, got {getattr(t, 'dtype', type(t).__name__)}")
-    if t.dim() < 1 or t.shape[-1] < 1:
-        raise ValueError(f"{name} must have shape [..., M] with M >= 1, got {tuple(t.shape)}")
+    shape = t.shape
+    if not shape or shape[-1] < 1:
+        raise ValueError(f"{name} must have shape [..., M] with M >= 1, got {tuple(shape)}")
     if not t.is_cuda:
         raise ValueError("libtp runs on CUDA tensors only (no CPU fallback)")
-    M = t.shape[-1]
-    if t.dim() == 2 and t.stride(1) == 1:
-        strides = (t.shape[0], t.stride(0), 0)
-    else:
-        strides = _row_strides(t)
+    M = shape[-1]
+    if len(shape) == 2:
+        row, one = t.stride()
+        if one == 1 or M == 1:
+            return _lib.tp_rows(kind, shape[0], M, shape[0], row, 0, t.data_ptr()), t
+    strides = _row_strides(t)
     if strides is None:
         if not copy:
             raise ValueError(f"{name}: its rows must be contiguous and lie at one stride, or at two")
         t = t.contiguous()
         strides = (t.numel() // M, M, 0)
-    return _lib.tp_rows(_ROWS_DT[t.dtype], t.numel() // M, M, *strides, t.data_ptr()), t
+    return _lib.tp_rows(kind, t.numel() // M, M, *strides, t.data_ptr()), t
 
 
 def _side(t, dtype, name, shape, like):
@@ -342,7 +345,7 @@ def _side(t, dtype, name, shape, like):
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         whole = not (t.dtype.is_floating_point or t.dtype.is_complex or t.dtype == torch.bool)
         if not (whole if dtype == torch.int64 else t.dtype.is_floating_point):
             raise TypeError(f"{name} must be {'an integer' if dtype == torch.int64 else 'a floating-point'} tensor, got {t.dtype}")
@@ -379,17 +382,19 @@ def token_logprobs(logits, tokens, temperature: float = 1.0, top: int = 0, want_
     r, logits = _rows(logits)
     lead, dev = logits.shape[:-1], logits.device
     tokens = _side(tokens, torch.int64, "tokens", lead, logits)
-    top = int(top)
-    if top < 0 or top > min(r.M, 128):
+    if top < 0 or top > 128 or top > r.M:
         raise ValueError(f"top must be in [0, min(M, 128)], got {top}")
-    f32 = {"dtype": torch.float32, "device": dev}
-    entropy = torch.empty(lead, **f32)
-    logprobs = None if tokens is None else torch.empty(lead, **f32)
-    topv = torch.empty((*lead, top), **f32) if top else None
-    topi = torch.empty((*lead, top), dtype=torch.int64, device=dev) if top else None
-    stats = torch.empty((r.N, STATS), **f32) if want_stats else None
+    entropy = torch.empty(lead, dtype=torch.float32, device=dev)
+    logprobs = topv = topi = stats = None
+    if tokens is not None:
+        logprobs = torch.empty(lead, dtype=torch.float32, device=dev)
+    if top:
+        topv = torch.empty((*lead, top), dtype=torch.float32, device=dev)
+        topi = torch.empty((*lead, top), dtype=torch.int64, device=dev)
+    if want_stats:
+        stats = torch.empty((r.N, STATS), dtype=torch.float32, device=dev)
     if r.N:
-        _launch("tp_token_logprobs", dev, r, _p(tokens), float(temperature), top, _p(logprobs), _p(entropy), _p(stats),
+        _launch("tp_token_logprobs", dev, r, _p(tokens), temperature, top, _p(logprobs), entropy.data_ptr(), _p(stats),
                 _p(topv), _p(topi))
     return logprobs, entropy, topv, topi, stats
 
@@ -401,11 +406,21 @@ def token_logprobs_backward(logits, tokens, temperature, stats, grad_logprobs, g
     stats = _side(stats, torch.float32, "stats", (r.N, STATS), logits)
     g1 = _side(grad_logprobs, torch.float32, "grad_logprobs", lead, logits)
     g2 = _side(grad_entropy, torch.float32, "grad_entropy", lead, logits)
+    return _logprobs_grad(logits, r, tokens, temperature, stats, g1, g2)
+
+
+def _logprobs_grad(logits, r, tokens, temperature, stats, g1, g2):
+    """The gradient from arguments that are known to be in order (what autograd kept of the forward)."""
     grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
     if r.N:
-        _launch("tp_token_logprobs_backward", logits.device, r, _p(tokens), float(temperature), _p(stats), _p(g1), _p(g2),
-                _rows(grad)[0])
+        _launch("tp_token_logprobs_backward", logits.device, r, _p(tokens), temperature, stats.data_ptr(), _p(g1), _p(g2),
+                _dense(r, grad))
     return grad
+
+
+def _dense(r, t):
+    """The tp_rows of a contiguous tensor of the shape and type of r's."""
+    return _lib.tp_rows(r.dtype, r.N, r.M, r.N, r.M, 0, t.data_ptr())
 
 
 def _teacher(logits, r, ids, values):
@@ -426,8 +441,8 @@ def topk_distillation(logits, teacher_ids, teacher_values, temperature: float = 
     loss = torch.empty(logits.shape[:-1], dtype=torch.float32, device=logits.device)
     stats = torch.empty((r.N, STATS), dtype=torch.float32, device=logits.device) if want_stats else None
     if r.N:
-        _launch("tp_topk_distillation", logits.device, r, K, _p(ids), _p(values), float(temperature), int(bool(rest)),
-                _p(loss), _p(stats))
+        _launch("tp_topk_distillation", logits.device, r, K, ids.data_ptr(), values.data_ptr(), temperature, bool(rest),
+                loss.data_ptr(), _p(stats))
     return loss, stats
 
 
@@ -436,10 +451,15 @@ def topk_distillation_backward(logits, teacher_ids, teacher_values, temperature,
     K, ids, values = _teacher(logits, r, teacher_ids, teacher_values)
     stats = _side(stats, torch.float32, "stats", (r.N, STATS), logits)
     gl = _side(grad_loss, torch.float32, "grad_loss", logits.shape[:-1], logits)
+    return _distillation_grad(logits, r, ids, values, temperature, rest, stats, gl)
+
+
+def _distillation_grad(logits, r, ids, values, temperature, rest, stats, gl):
+    """The gradient from arguments that are known to be in order (what autograd kept of the forward)."""
     grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
     if r.N:
-        _launch("tp_topk_distillation_backward", logits.device, r, K, _p(ids), _p(values), float(temperature),
-                int(bool(rest)), _p(stats), _p(gl), _rows(grad)[0])
+        _launch("tp_topk_distillation_backward", logits.device, r, ids.shape[-1], ids.data_ptr(), values.data_ptr(),
+                temperature, bool(rest), stats.data_ptr(), gl.data_ptr(), _dense(r, grad))
     return grad
 
 
@@ -448,15 +468,18 @@ def topk_distillation_grad(logits, teacher_ids, teacher_values, weights=None, te
     given = logits
     r, logits = _rows(logits)
     K, ids, values = _teacher(logits, r, teacher_ids, teacher_values)
+    dev = logits.device
     weights = _side(weights, torch.float32, "weights", logits.shape[:-1], logits)
     if out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-    elif out.shape != given.shape or out.dtype != given.dtype or out.device != given.device:
-        raise ValueError("out must have the logits' shape, dtype and device")
-    g = _rows(out, "out", copy=False)[0]
-    loss = torch.empty(logits.shape[:-1], dtype=torch.float32, device=logits.device)
-    stats = torch.empty((r.N, STATS), dtype=torch.float32, device=logits.device)
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+        g = _dense(r, out)
+    else:
+        if out.shape != given.shape or out.dtype != given.dtype or out.device != given.device:
+            raise ValueError("out must have the logits' shape, dtype and device")
+        g = _rows(out, "out", copy=False)[0]
+    loss = torch.empty(logits.shape[:-1], dtype=torch.float32, device=dev)
+    stats = torch.empty((r.N, STATS), dtype=torch.float32, device=dev)
     if r.N:
-        _launch("tp_topk_distillation_grad", logits.device, r, K, _p(ids), _p(values), _p(weights), float(temperature),
-                int(bool(rest)), _p(loss), _p(stats), g)
+        _launch("tp_topk_distillation_grad", dev, r, K, ids.data_ptr(), values.data_ptr(), _p(weights), temperature,
+                bool(rest), loss.data_ptr(), stats.data_ptr(), g)
     return loss, out
