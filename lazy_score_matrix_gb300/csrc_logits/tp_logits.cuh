@@ -556,23 +556,22 @@ struct Marks {
     }
 };
 
-// The thread's state of the slice's columns; of the unlisted ones where REST.
+// The thread's state of the slice's columns; of the unlisted ones where REST. next: the thread's first chunk.
 template <class T, int TEAM, bool REST>
 __device__ __forceinline__ State read_slice(const DistillArgs& a, const RowVecs<T>& x, const Slice& sl, const ListBuf& list,
-                                            Marks<TEAM>& marks) {
+                                            Marks<TEAM>& marks, uint4 (&next)[kUnroll]) {
     constexpr int V = Elem<T>::kVec, kMarkVecs = Marks<TEAM>::kCols / V;
     const int t = Team<TEAM>::tid();
     State st;
     for (int part = sl.begin; part < sl.end; part += REST ? kMarkVecs : sl.end) {
         const int end = REST ? min(sl.end, part + kMarkVecs) : sl.end;
-        uint4 next[kUnroll];  // a chunk is under way while the one before it is reduced
-        x.load(next, part + t, TEAM, end);
+        if (part != sl.begin) x.load(next, part + t, TEAM, end);
         if (REST) marks.set(list, a.K, x.first(part), (end - part) * V);
         for (int base = part; base < end; base += TEAM * kUnroll) {
             uint4 r[kUnroll];
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) r[u] = next[u];
-            x.load(next, base + TEAM * kUnroll + t, TEAM, end);
+            x.load(next, base + TEAM * kUnroll + t, TEAM, end);  // under way while this one is reduced
             if (REST) {
 #pragma unroll
                 for (int u = 0; u < kUnroll; ++u) {

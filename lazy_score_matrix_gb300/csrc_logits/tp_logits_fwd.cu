@@ -324,9 +324,11 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const DistillArgs 
     if (size > 1) cluster_arrive();
     const RowVecs<T> x(p, a.x.M);
     const Slice sl = slice_of(x.n, rank, size);
+    uint4 next[kUnroll];
+    x.load(next, sl.begin + t, TEAM, sl.end);
     look_up<T, TEAM>(a, p, list, 0, a.x.M);
     if (rank == 0 && (TEAM == 32 || threadIdx.x < 32)) sum_list(a, list);
-    State st = read_slice<T, TEAM, REST>(a, x, sl, list, marks[REST ? Tm::id() : 0]);
+    State st = read_slice<T, TEAM, REST>(a, x, sl, list, marks[REST ? Tm::id() : 0], next);
     st = team_state<TEAM>(st, a.sc.c, red);
     if (size > 1) {
         cluster_wait();  // every CTA of the cluster runs

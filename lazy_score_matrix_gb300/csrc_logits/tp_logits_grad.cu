@@ -141,7 +141,9 @@ __global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillArg
         zero_range<T, TEAM>(o, e0, e1);
         return;
     }
-    distill_row_grad<T, TEAM, false>(a, s, w, o, e0, e1, from_slice<T>(buf, s0, n, o));
+    const Source<T> from = from_slice<T>(buf, s0, n, o);
+    Fetch<T, TEAM, false> scores(o, e0, e1, from);
+    distill_row_grad<T, TEAM, false>(a, s, w, o, e0, e1, scores);
     Tm::sync();
     distill_list_grad<T, TEAM>(a, s, w, o, e0, e1, list, twice);
 }
@@ -172,10 +174,14 @@ __global__ void __launch_bounds__(kLongThreads, 2) distill_grad_long_kernel(cons
         }
         return zero_range<T, TEAM>(o, 0, M);
     }
+    const RowVecs<T> x(p, M);
+    uint4 next[kUnroll];
+    x.load(next, threadIdx.x, TEAM, x.n);
     const bool twice = look_up<T, TEAM>(a, p, list, 0, M);
     if (threadIdx.x < 32) sum_list(a, list);
-    const RowVecs<T> x(p, M);
-    State st = read_slice<T, TEAM, REST>(a, x, Slice{0, x.n}, list, marks[0]);
+    State st = read_slice<T, TEAM, REST>(a, x, Slice{0, x.n}, list, marks[0], next);
+    const Source<T> from = from_row<T>(p, M, o);
+    Fetch<T, TEAM, true> scores(o, 0, M, from);  // the second reading begins while the states meet
     st = team_state<TEAM>(st, a.sc.c, red);
     if (threadIdx.x < 32) {
         const RowStats s = close_row(a, st, list);
@@ -191,7 +197,7 @@ __global__ void __launch_bounds__(kLongThreads, 2) distill_grad_long_kernel(cons
     const RowStats s = shared_stats;
     if (s.m == neg_inf()) return zero_range<T, TEAM>(o, 0, M);  // a row of -inf alone
     const float w = (a.weights ? a.weights[row] : 1.f) * a.sc.inv;
-    distill_row_grad<T, TEAM, true>(a, s, w, o, 0, M, from_row<T>(p, M, o));
+    distill_row_grad<T, TEAM, true>(a, s, w, o, 0, M, scores);
     __syncthreads();
     distill_list_grad<T, TEAM>(a, s, w, o, 0, M, list, twice);
 }

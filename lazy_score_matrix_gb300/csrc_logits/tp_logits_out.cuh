@@ -51,32 +51,52 @@ __device__ __forceinline__ Source<T> from_row(const T* p, int M, const T* o) {
     return s;
 }
 
+// The whole vectors of a range of the gradient row o, and the first chunk of their scores, under way.
+template <class T, int TEAM, bool STREAM>
+struct Fetch {
+    static constexpr int V = Elem<T>::kVec;
+    const Source<T>& from;
+    int off, ja, jb;
+    uint4 next[kUnroll];
+    __device__ __forceinline__ Fetch(const T* o, int e0, int e1, const Source<T>& from_) : from(from_), off(off_of(o)) {
+        ja = max((e0 + off + V - 1) / V, from.lo), jb = max(ja, min((e1 + off) / V, from.hi));
+        if (STREAM) load(ja + Team<TEAM>::tid());  // shared memory needs no head start
+    }
+    __device__ __forceinline__ void load(int j) {
+        if (j + (kUnroll - 1) * TEAM < jb) {
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) next[u] = from.template get<STREAM>(j + u * TEAM);
+        } else {
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (j + u * TEAM < jb) next[u] = from.template get<STREAM>(j + u * TEAM);
+        }
+    }
+};
+
 // o[e] = f(score e) for e0 <= e < e1. f(float[V], e) turns the scores of e .. e + V - 1 into gradients. Whole
 // vectors are written as such; what e0, e1 or the source's ends cut is done element by element.
 template <class T, int TEAM, bool STREAM, class F>
-__device__ __forceinline__ void map_range(T* o, int e0, int e1, const Source<T>& from, F f) {
+__device__ __forceinline__ void map_range(T* o, int e0, int e1, Fetch<T, TEAM, STREAM>& x, F f) {
     constexpr int V = Elem<T>::kVec;
-    const int off = off_of(o), t = Team<TEAM>::tid();
-    const int ja = max((e0 + off + V - 1) / V, from.lo), jb = max(ja, min((e1 + off) / V, from.hi));
+    const int off = x.off, t = Team<TEAM>::tid(), ja = x.ja, jb = x.jb;
+    const Source<T>& from = x.from;
     uint4* out = reinterpret_cast<uint4*>(o - off);
-    int j = ja + t;
-    for (; j + (kUnroll - 1) * TEAM < jb; j += TEAM * kUnroll) {
+    for (int j = ja + t; j < jb; j += TEAM * kUnroll) {
         uint4 r[kUnroll];
+        if (!STREAM) x.load(j);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) r[u] = from.template get<STREAM>(j + u * TEAM);
+        for (int u = 0; u < kUnroll; ++u) r[u] = x.next[u];
+        if (STREAM) x.load(j + TEAM * kUnroll);
+        const bool all = j + (kUnroll - 1) * TEAM < jb;
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
+            if (!all && j + u * TEAM >= jb) break;
             float v[V];
             Elem<T>::unpack(r[u], v);
             f(v, (j + u * TEAM) * V - off);
             __stcs(out + j + u * TEAM, Elem<T>::pack(v));
         }
-    }
-    for (; j < jb; j += TEAM) {
-        float v[V];
-        Elem<T>::unpack(from.template get<STREAM>(j), v);
-        f(v, j * V - off);
-        __stcs(out + j, Elem<T>::pack(v));
     }
     const int head = min(e1, ja * V - off), tail = max(head, jb * V - off);
     const auto one = [&](int e) {
@@ -138,9 +158,9 @@ __device__ __forceinline__ void shares(const DistillArgs& a, ListBuf& l) {
 // Gradient of the columns from e0 to e1 as if none were listed; w: the row's weight over T.
 template <class T, int TEAM, bool STREAM>
 __device__ __forceinline__ void distill_row_grad(const DistillArgs& a, const RowStats& s, float w, T* o, int e0, int e1,
-                                                 const Source<T>& from) {
+                                                 Fetch<T, TEAM, STREAM>& x) {
     const float coef = s.coef * w, gm = s.gm, gls2 = s.gls * kLog2e, c = a.sc.c;
-    map_range<T, TEAM, STREAM>(o, e0, e1, from, [&](float* f, int) {
+    map_range<T, TEAM, STREAM>(o, e0, e1, x, [&](float* f, int) {
 #pragma unroll
         for (int i = 0; i < Elem<T>::kVec; ++i) f[i] = coef * ex2(fmaf(f[i] - gm, c, -gls2));
     });
