@@ -36,7 +36,7 @@ struct Scale {
 
 struct LogprobArgs {
     View x;
-    int64_t N;
+    int64_t N, under_way;  // under_way: rows that the card works on at a time
     const int64_t* tokens;
     Scale sc;
     int top;
@@ -49,7 +49,7 @@ struct LogprobArgs {
 
 struct DistillArgs {
     View x;
-    int64_t N;
+    int64_t N, under_way;
     const int64_t* ids;
     const float* values;
     int K, rest;

@@ -2,8 +2,6 @@
 // softmax state in registers; the alternatives are filtered in the same pass.
 #include <cuda_runtime.h>
 
-#include <atomic>
-
 #include "tp_launch.h"
 #include "tp_logits.cuh"
 
@@ -11,31 +9,37 @@ namespace tp {
 namespace rows {
 namespace {
 
-// Alternatives. When a row has been read once, the top-th largest of its threads' own maxima bounds the top-th
-// largest score from below: that many threads hold a column that reaches it. A second reading of the row, from
-// the cache, collects the columns that reach the bound; of 128K columns under 512 threads that is about 1.2 times
-// `top`. They are ranked by counting, each against all others. Where ties let more columns through than the
-// buffer holds, it is cut back to the best ones by bisection and the bound becomes a key (value and column).
+// Alternatives. While a row is read, every thread notes the largest score of each of its chunks. When it has been
+// read, the top-th largest of the threads' own maxima bounds the top-th largest score from below: that many
+// threads hold a column that reaches it. Only the chunks whose maximum reaches the bound are looked at again, about
+// 1.2 times `top` of the 2048 of a row of 64K columns, spread evenly over the threads, and their columns
+// that reach it are ranked by counting, each against all others. Where ties let through more chunks or columns
+// than there is room for, the whole row is read again and the columns cut back to the best ones by bisection; the
+// bound then becomes a key (value and column).
 template <int TEAM>
 struct TopBuf {
-    static constexpr int kCap = TEAM == 32 ? 256 : 2048, kKeep = TEAM == 32 ? 96 : kCap / kMaxCluster;
+    static constexpr int kKeep = TEAM == 32 ? 96 : kMaxList + 32;       // keys after a cut, at most
+    static constexpr int kCap = TEAM == 32 ? 256 : kMaxCluster * kKeep;  // room for what a cluster's CTAs keep
+    static constexpr int kSlots = TEAM == kLongThreads ? 8 : 16, kWork = TEAM == 32 ? 128 : 1024;
     unsigned long long key[kCap];
     unsigned long long thr;  // keys at or below it cannot be among the best
-    int cnt;
+    float chunk[kSlots][TEAM];      // largest score of the thread's chunks, `each` of them to a slot
+    unsigned short work[kWork];     // slots to look at again: slot * TEAM + thread
+    int cnt, todo;
     uint32_t slot[3];  // reductions of a CTA, in turn: one in use, one read, one cleared
 };
 
 template <int TEAM>
 struct Tops {
     using Buf = TopBuf<TEAM>;
-    static constexpr int kPer = Buf::kCap / TEAM;  // keys a thread looks at
+    static constexpr int kPer = (Buf::kCap + TEAM - 1) / TEAM;  // keys a thread looks at
     Buf& b;
     const int top;
     int turn = 0;
 
     __device__ __forceinline__ Tops(Buf& b_, int top_) : b(b_), top(top_) {}
     __device__ __forceinline__ void clear() {
-        if (Team<TEAM>::tid() == 0) b.cnt = 0, b.thr = 0, b.slot[0] = b.slot[1] = b.slot[2] = 0;
+        if (Team<TEAM>::tid() == 0) b.cnt = b.todo = 0, b.thr = 0, b.slot[0] = b.slot[1] = b.slot[2] = 0;
         Team<TEAM>::sync();
     }
     template <class Op, class Warp>
@@ -111,27 +115,36 @@ struct Tops {
         const uint32_t o = ::max((uint32_t)(thr >> 32), ord_of(lowest()));  // a bound may lie below every finite value
         return of_ord(~(uint32_t)thr < (uint32_t)col ? o + 1 : o);
     }
-    // The columns of this thread's vectors (vector u at column col0 + u step) that reach the bar, to the buffer as
-    // long as it has room; cnt counts them all.
-    template <class T, int N>
-    __device__ __forceinline__ void collect(const uint4 (&r)[N], int col0, int step, float bar) {
+    // The columns that reach the bar, to the buffer, by way of the chunks that do. false: there was not room for all.
+    // Slots hold `each` chunks; the slice begins at vector `begin`.
+    template <class T>
+    __device__ __forceinline__ bool collect(const RowVecs<T>& x, int begin, int end, int each, float bar) {
         constexpr int V = Elem<T>::kVec;
-        const auto type_bar = Elem<T>::bar(bar);
-#pragma unroll
-        for (int u = 0; u < N; ++u)
-            if (Elem<T>::reaches(r[u], type_bar)) {  // few do
-                float f[V];
-                Elem<T>::unpack(r[u], f);
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (f[i] >= bar) {
-                        const int at = atomicAdd(&b.cnt, 1);
-                        if (at < Buf::kCap) b.key[at] = key_of(f[i], col0 + u * step + i);
-                    }
+        const int t = Team<TEAM>::tid(), chunk = TEAM * kUnroll, slots = (end - begin + each * chunk - 1) / (each * chunk);
+        for (int i = 0; i < slots; ++i)
+            if (b.chunk[i][t] >= bar) {
+                const int at = atomicAdd(&b.todo, 1);
+                if (at < Buf::kWork) b.work[at] = (unsigned short)(i * TEAM + t);
             }
+        Team<TEAM>::sync();
+        const int vecs = each * kUnroll, n = min(b.todo, Buf::kWork) * vecs;
+        for (int i = t; i < n; i += TEAM) {
+            const int w = b.work[i / vecs], j = begin + w / TEAM * each * chunk + i % vecs * TEAM + w % TEAM;
+            if (j >= end) continue;
+            float f[V];
+            Elem<T>::unpack(x.inside(j) ? __ldcg(x.base + j) : x.edge(j), f);
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                if (f[k] >= bar) {
+                    const int at = atomicAdd(&b.cnt, 1);
+                    if (at < Buf::kCap) b.key[at] = key_of(f[k], x.first(j) + k);
+                }
+        }
+        Team<TEAM>::sync();
+        return b.todo <= Buf::kWork && b.cnt <= Buf::kCap;
     }
-    // The same for a row of more of them than the buffer holds: the whole team calls it, and cuts the buffer back
-    // whenever it is full.
+    // The columns of this thread's vectors (vector u at column col0 + u step of the row p) that reach the bar, to the
+    // buffer, which is cut back whenever it is full. The whole team calls it.
     template <class T, int N>
     __device__ __forceinline__ void offer(const uint4 (&r)[N], const T* p, int col0, int step, float bar) {
         constexpr int V = Elem<T>::kVec;
@@ -174,7 +187,7 @@ __device__ __forceinline__ void leave_out(const LogprobArgs& a, int64_t row, int
 }
 
 struct Gather {  // the candidates of a cluster's CTAs, in the first of them
-    static constexpr int kMost = TopBuf<kThreads>::kKeep;
+    static constexpr int kMost = TopBuf<kLongThreads>::kKeep;
     unsigned long long key[kMaxCluster][kMost];
     int n[kMaxCluster];
 };
@@ -188,7 +201,9 @@ __global__ void __launch_bounds__(TEAM == 32 ? kThreads : TEAM, TEAM == kLongThr
     __shared__ TopBuf<TEAM> tops[TOP ? Tm::kPerCta : 1];
     __shared__ Gather others[1];
     __shared__ uint32_t bounds[kMaxCluster];
-    const int rank = TEAM == 32 ? 0 : cluster_rank(), size = TEAM == 32 ? 1 : cluster_size();
+    // clusters: the kernels of kLongThreads with alternatives, all of a CTA a row without
+    constexpr bool kCluster = TEAM == kLongThreads || (TEAM != 32 && !TOP);
+    const int rank = kCluster ? cluster_rank() : 0, size = kCluster ? cluster_size() : 1;
     const int64_t row = TEAM == 32 ? (int64_t)blockIdx.x * Tm::kPerCta + Tm::id() : blockIdx.x / size;
     if (row >= a.N) return;
     const int t = Tm::tid();
@@ -201,15 +216,26 @@ __global__ void __launch_bounds__(TEAM == 32 ? kThreads : TEAM, TEAM == kLongThr
     const RowVecs<T> x(row_at<const T>(a.x, row), a.x.M);
     const Slice sl = slice_of(x.n, rank, size);
     State st;
+    const int chunks = (sl.end - sl.begin + TEAM * kUnroll - 1) / (TEAM * kUnroll);
+    const int each = max(1, (chunks + TopBuf<TEAM>::kSlots - 1) / TopBuf<TEAM>::kSlots);  // chunks to a slot
+    int slot = 0, in_slot = 0;
+    float noted = neg_inf();
     uint4 next[kUnroll];  // a chunk is under way while the one before it is reduced
     x.load(next, sl.begin + t, TEAM, sl.end);
+    if (TEAM != 32 && t == 0) x.ahead(sl.begin + TEAM * kUnroll, TEAM * kUnroll, sl.end, true);
     for (int base = sl.begin; base < sl.end; base += TEAM * kUnroll) {
         uint4 r[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) r[u] = next[u];
         x.load(next, base + TEAM * kUnroll + t, TEAM, sl.end);
-        add_scores<T, true>(st, r, a.sc);
+        if (TEAM != 32 && t == 0) x.ahead(base + TEAM * kUnroll, TEAM * kUnroll, sl.end);
+        const float here = add_scores<T, true>(st, r, a.sc);
+        if (TOP) {
+            noted = max_nan(noted, here);
+            if (++in_slot == each || base + TEAM * kUnroll >= sl.end) tops[Tm::id()].chunk[slot++][t] = noted, noted = neg_inf(), in_slot = 0;
+        }
     }
+    if (!TOP && TEAM != 32 && t == 0) begin_row<T>(a.x, a.N, row + a.under_way, TEAM * kUnroll);
     const float own = st.m;
     st = team_state<TEAM>(st, a.sc.c, red);
     Tops<TEAM> best(tops[TOP ? Tm::id() : 0], a.top);
@@ -230,17 +256,7 @@ __global__ void __launch_bounds__(TEAM == 32 ? kThreads : TEAM, TEAM == kLongThr
             for (int r = 0; r < size; ++r) bound = max(bound, bounds[r]);  // each holds for the whole row
     }
     if (TOP) {
-        const float bar = bound ? of_ord(bound) : lowest();
-        x.load(next, sl.begin + t, TEAM, sl.end);
-        for (int base = sl.begin; base < sl.end; base += TEAM * kUnroll) {
-            uint4 r[kUnroll];
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) r[u] = next[u];
-            x.load(next, base + TEAM * kUnroll + t, TEAM, sl.end);
-            best.template collect<T>(r, x.first(base + t), TEAM * V, bar);
-        }
-        Tm::sync();
-        if (best.b.cnt > TopBuf<TEAM>::kCap) {
+        if (!best.template collect<T>(x, sl.begin, sl.end, each, bound ? of_ord(bound) : lowest())) {
             Tm::sync();
             if (t == 0) best.b.cnt = 0, best.b.thr = bound ? ((unsigned long long)bound << 32) - 1 : 0;
             Tm::sync();
@@ -326,6 +342,7 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const DistillArgs 
     const Slice sl = slice_of(x.n, rank, size);
     uint4 next[kUnroll];
     x.load(next, sl.begin + t, TEAM, sl.end);
+    if (TEAM != 32 && t == 0) x.ahead(sl.begin + TEAM * kUnroll, TEAM * kUnroll, sl.end, true);
     look_up<T, TEAM>(a, p, list, 0, a.x.M);
     if (rank == 0 && (TEAM == 32 || threadIdx.x < 32)) sum_list(a, list);
     State st = read_slice<T, TEAM, REST>(a, x, sl, list, marks[REST ? Tm::id() : 0], next);
@@ -355,24 +372,20 @@ template <class T>
 constexpr int64_t kChunk = kThreads * kUnroll * Elem<T>::kVec;
 
 template <class T>
-void run_logprobs(const LogprobArgs& a, cudaStream_t s) {
+void run_logprobs(LogprobArgs a, cudaStream_t s) {
     HookScope h("token_logprobs", s);
     Shape sh = shape_of(a.N, a.x.M, a.top <= 32, kChunk<T>);
-    const int64_t row = (int64_t)a.x.M * (int64_t)sizeof(T);
+    a.under_way = 4 * kSms;
     if (sh.warp) {
         if (a.top) launch(logprobs_kernel<T, 32, true>, sh, s, a);
         else launch(logprobs_kernel<T, 32, false>, sh, s, a);
-    } else if (a.top && sh.cluster == 1 && 4 * kSms * row <= kCacheBytes) {
-        launch(logprobs_kernel<T, kThreads, true>, sh, s, a);
-    } else if (a.top) {
-        auto kernel = logprobs_kernel<T, kLongThreads, true>;
-        static std::atomic<uint64_t> ready{0};
-        sh.threads = kLongThreads;
-        if (sh.cluster == 1 && a.N > kSms && 2 * kSms * row > kCacheBytes) sh.smem = kAlone;
-        if (sh.smem && !raise_smem(kernel, kAlone, ready)) return;
-        launch(kernel, sh, s, a);
-    } else {
+    } else if (!a.top) {
         launch(logprobs_kernel<T, kThreads, false>, sh, s, a);
+    } else if (sh.cluster == 1 && a.N >= kFewRows) {
+        launch(logprobs_kernel<T, kThreads, true>, sh, s, a);
+    } else {
+        sh.threads = kLongThreads;
+        launch(logprobs_kernel<T, kLongThreads, true>, sh, s, a);
     }
 }
 template <class T>

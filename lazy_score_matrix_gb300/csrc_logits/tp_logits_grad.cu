@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(kLongThreads, 2) distill_grad_long_kernel(cons
     const RowVecs<T> x(p, M);
     uint4 next[kUnroll];
     x.load(next, threadIdx.x, TEAM, x.n);
+    if (threadIdx.x == 0) x.ahead(TEAM * kUnroll, TEAM * kUnroll, x.n, true);
     const bool twice = look_up<T, TEAM>(a, p, list, 0, M);
     if (threadIdx.x < 32) sum_list(a, list);
     State st = read_slice<T, TEAM, REST>(a, x, Slice{0, x.n}, list, marks[0], next);
@@ -198,12 +199,13 @@ __global__ void __launch_bounds__(kLongThreads, 2) distill_grad_long_kernel(cons
     if (s.m == neg_inf()) return zero_range<T, TEAM>(o, 0, M);  // a row of -inf alone
     const float w = (a.weights ? a.weights[row] : 1.f) * a.sc.inv;
     distill_row_grad<T, TEAM, true>(a, s, w, o, 0, M, scores);
+    if (threadIdx.x == 0) begin_row<T>(a.x, a.N, row + a.under_way, TEAM * kUnroll);
     __syncthreads();
     distill_list_grad<T, TEAM>(a, s, w, o, 0, M, list, twice);
 }
 
 template <class T, bool REST>
-void go_long(const DistillArgs& a, cudaStream_t s) {
+void go_long(DistillArgs a, cudaStream_t s) {
     auto kernel = distill_grad_long_kernel<T, REST>;
     static std::atomic<uint64_t> ready{0};
     if (!raise_smem(kernel, kAlone, ready)) return;
@@ -214,6 +216,7 @@ void go_long(const DistillArgs& a, cudaStream_t s) {
     sh.grid = (unsigned)a.N;
     // two CTAs an SM by their registers, or one by its shared memory
     sh.smem = 2 * kSms * (int64_t)a.x.M * (int64_t)sizeof(T) <= kCacheBytes ? 0 : kAlone;
+    a.under_way = kSms * (sh.smem ? 1 : 2);
     HookScope h("topk_distillation_grad", s);
     launch(kernel, sh, s, a);
 }
