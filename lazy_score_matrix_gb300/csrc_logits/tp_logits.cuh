@@ -140,8 +140,10 @@ struct Elem<__nv_bfloat16> {
 
 template <class T>
 __device__ __forceinline__ T* row_at(const View& r, int64_t i) {
+    T* p = static_cast<T*>(r.data);
+    if (!r.grouped) return p + i * r.row_stride;
     const int64_t g = (uint32_t)i / (uint32_t)r.group;
-    return static_cast<T*>(r.data) + g * r.group_stride + (i - g * r.group) * r.row_stride;
+    return p + g * r.group_stride + (i - g * r.group) * r.row_stride;
 }
 
 // A row as 16-byte vectors: vector j covers elements j V - off .. j V - off + V - 1, where off is the row's
@@ -593,7 +595,7 @@ __device__ __forceinline__ State read_slice(const DistillArgs& a, const RowVecs<
             uint4 r[kUnroll];
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) r[u] = next[u];
-            x.load(next, base + TEAM * kUnroll + t, TEAM, end);  // under way while this one is reduced
+            if (base + TEAM * kUnroll < end) x.load(next, base + TEAM * kUnroll + t, TEAM, end);  // under way while this one is reduced
             if (TEAM != 32 && t == 0) x.ahead(base + TEAM * kUnroll, TEAM * kUnroll, sl.end);
             if (REST) {
 #pragma unroll

@@ -114,6 +114,7 @@ View view(const tp_rows* r) {
     v.group_stride = r->group < r->N ? r->group_stride : 0;
     v.M = (int)r->M;
     v.group = (int)r->group;
+    v.grouped = r->group < r->N;
     return v;
 }
 

@@ -23,6 +23,7 @@ struct View {
     void* data;
     int64_t row_stride, group_stride;
     int M, group;
+    bool grouped;  // more than one group
 };
 
 // The temperature as the kernels use it. c = log2(e)/T rounded to fp32 (exponents are 2^(c d)); its rounding is a

@@ -127,18 +127,20 @@ struct Tops {
                 if (at < Buf::kWork) b.work[at] = (unsigned short)(i * TEAM + t);
             }
         Team<TEAM>::sync();
-        const int vecs = each * kUnroll, n = min(b.todo, Buf::kWork) * vecs;
-        for (int i = t; i < n; i += TEAM) {
-            const int w = b.work[i / vecs], j = begin + w / TEAM * each * chunk + i % vecs * TEAM + w % TEAM;
-            if (j >= end) continue;
-            float f[V];
-            Elem<T>::unpack(x.inside(j) ? __ldcg(x.base + j) : x.edge(j), f);
+        const int n = min(b.todo, Buf::kWork), lane = t % kUnroll * TEAM;
+        for (int i = t / kUnroll; i < n; i += TEAM / kUnroll) {
+            const int w = b.work[i];
+            int j = begin + w / TEAM * each * chunk + w % TEAM + lane;
+            for (int c = 0; c < each && j < end; ++c, j += chunk) {
+                float f[V];
+                Elem<T>::unpack(x.inside(j) ? __ldcg(x.base + j) : x.edge(j), f);
 #pragma unroll
-            for (int k = 0; k < V; ++k)
-                if (f[k] >= bar) {
-                    const int at = atomicAdd(&b.cnt, 1);
-                    if (at < Buf::kCap) b.key[at] = key_of(f[k], x.first(j) + k);
-                }
+                for (int k = 0; k < V; ++k)
+                    if (f[k] >= bar) {
+                        const int at = atomicAdd(&b.cnt, 1);
+                        if (at < Buf::kCap) b.key[at] = key_of(f[k], x.first(j) + k);
+                    }
+            }
         }
         Team<TEAM>::sync();
         return b.todo <= Buf::kWork && b.cnt <= Buf::kCap;
@@ -227,7 +229,7 @@ __global__ void __launch_bounds__(TEAM == 32 ? kThreads : TEAM, TEAM == kLongThr
         uint4 r[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) r[u] = next[u];
-        x.load(next, base + TEAM * kUnroll + t, TEAM, sl.end);
+        if (base + TEAM * kUnroll < sl.end) x.load(next, base + TEAM * kUnroll + t, TEAM, sl.end);
         if (TEAM != 32 && t == 0) x.ahead(base + TEAM * kUnroll, TEAM * kUnroll, sl.end);
         const float here = add_scores<T, true>(st, r, a.sc);
         if (TOP) {
