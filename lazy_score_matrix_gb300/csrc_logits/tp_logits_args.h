@@ -70,16 +70,19 @@ struct Shape {
     size_t smem = 0;
 };
 constexpr int64_t kSms = 152;
-constexpr int64_t kWarpCols = 4096, kWarpRows = kSms * 8;
-constexpr int64_t kFewRows = kSms * 4;
+// A warp a row from so many rows on, up to so many bytes a row (a kernel that reads the row twice: half, so that the
+// 4864 rows under way fit the L2 cache). 12000 x 5000 bf16: forward 77 us with a CTA a row, 38 with a warp; 12000
+// x 12000: 91 and 68 us; 8192 x 32000: 97 and 110 us.
+constexpr int64_t kWarpRows = kSms * 8, kWarpBytes = 32 << 10;
+constexpr int64_t kResident = kSms * 4, kResidentLong = kSms * 2;  // CTAs of kThreads and of kLongThreads on the card
 
-// Many rows: one CTA a row, or, where a row is short, one warp a row. Few rows: up to 8 CTAs a row, as long as a
-// CTA keeps a chunk of `chunk` columns of its own.
-inline Shape shape_of(int64_t N, int64_t M, bool warps, int64_t chunk) {
+// Many rows of at most warp_bytes: one warp a row. Few rows: a cluster of up to 8 CTAs a row, as long as all of them
+// are resident at once (`resident` CTAs on the card) and each keeps 8 KB of the row or more. Else one CTA a row.
+inline Shape shape_of(int64_t N, int64_t row_bytes, int64_t warp_bytes, int64_t resident) {
     Shape s;
-    s.warp = warps && M <= kWarpCols && N >= kWarpRows;
+    s.warp = row_bytes <= warp_bytes && N >= kWarpRows;
     s.cluster = 1;
-    while (!s.warp && s.cluster < 8 && N * s.cluster < kFewRows && M >= 2 * s.cluster * chunk) s.cluster *= 2;
+    while (!s.warp && s.cluster < 8 && 2 * N * s.cluster <= resident && row_bytes >= 2 * s.cluster * (8 << 10)) s.cluster *= 2;
     s.grid = (unsigned)(s.warp ? (N + 7) / 8 : N * s.cluster);
     return s;
 }
@@ -96,12 +99,6 @@ inline bool raise_smem(K kernel, size_t bytes, std::atomic<uint64_t>& ready) {
     ready.fetch_or(bit, std::memory_order_relaxed);
     return true;
 }
-
-// Kernels that read a row twice want it in the L2 cache (129 MB) the second time: the rows under way on the whole
-// card may take so much of it. Where the CTAs that an SM's registers admit would have more, one is kept alone
-// on its SM by shared memory that it does not use.
-constexpr int64_t kCacheBytes = (int64_t)110 << 20;
-constexpr size_t kAlone = 120 * 1024;
 
 template <class... KArgs, class... Args>
 inline void launch(void (*kernel)(KArgs...), const Shape& sh, cudaStream_t s, const Args&... a) {

@@ -74,13 +74,10 @@ __global__ void __launch_bounds__(kThreads) distill_bwd_kernel(const DistillArgs
     distill_list_grad<T, TEAM>(a, s, w, o, r.e0, r.e1, list, twice);
 }
 
-// 16-byte vectors a CTA should keep when few rows are split
-constexpr int64_t kLeast = kThreads * kUnroll;
-
 template <class T>
 void run_logprobs(const LogprobArgs& a, cudaStream_t s) {
     HookScope h("token_logprobs_backward", s);
-    const Shape sh = shape_of(a.N, a.x.M, true, kLeast * Elem<T>::kVec);
+    const Shape sh = shape_of(a.N, (int64_t)a.x.M * (int64_t)sizeof(T), kWarpBytes, kResident);
     const int parts = sh.cluster;
     if (sh.warp) {
         if (a.g_entropy) logprobs_bwd_kernel<T, 32, true><<<sh.grid, kThreads, 0, s>>>(a, 1);
@@ -93,7 +90,7 @@ void run_logprobs(const LogprobArgs& a, cudaStream_t s) {
 template <class T>
 void run_distill(const DistillArgs& a, cudaStream_t s) {
     HookScope h("topk_distillation_backward", s);
-    const Shape sh = shape_of(a.N, a.x.M, true, kLeast * Elem<T>::kVec);
+    const Shape sh = shape_of(a.N, (int64_t)a.x.M * (int64_t)sizeof(T), kWarpBytes, kResident);
     if (sh.warp) distill_bwd_kernel<T, 32><<<sh.grid, kThreads, 0, s>>>(a, 1);
     else distill_bwd_kernel<T, kThreads><<<sh.grid, kThreads, 0, s>>>(a, sh.cluster);
 }

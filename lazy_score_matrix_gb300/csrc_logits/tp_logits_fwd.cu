@@ -371,19 +371,18 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const DistillArgs 
 }
 
 template <class T>
-constexpr int64_t kChunk = kThreads * kUnroll * Elem<T>::kVec;
-
-template <class T>
 void run_logprobs(LogprobArgs a, cudaStream_t s) {
     HookScope h("token_logprobs", s);
-    Shape sh = shape_of(a.N, a.x.M, a.top <= 32, kChunk<T>);
-    a.under_way = 4 * kSms;
+    const int64_t row = (int64_t)a.x.M * (int64_t)sizeof(T);
+    const bool large = a.top && a.N < kResident;  // few rows with alternatives: CTAs of kLongThreads
+    Shape sh = shape_of(a.N, row, a.top <= 32 ? kWarpBytes : 0, large ? kResidentLong : kResident);
+    a.under_way = kResident;
     if (sh.warp) {
         if (a.top) launch(logprobs_kernel<T, 32, true>, sh, s, a);
         else launch(logprobs_kernel<T, 32, false>, sh, s, a);
     } else if (!a.top) {
         launch(logprobs_kernel<T, kThreads, false>, sh, s, a);
-    } else if (sh.cluster == 1 && a.N >= kFewRows) {
+    } else if (!large) {
         launch(logprobs_kernel<T, kThreads, true>, sh, s, a);
     } else {
         sh.threads = kLongThreads;
@@ -393,7 +392,7 @@ void run_logprobs(LogprobArgs a, cudaStream_t s) {
 template <class T>
 void run_distill(const DistillArgs& a, cudaStream_t s) {
     HookScope h("topk_distillation", s);
-    const Shape sh = shape_of(a.N, a.x.M, true, kChunk<T>);
+    const Shape sh = shape_of(a.N, (int64_t)a.x.M * (int64_t)sizeof(T), kWarpBytes, kResident);
     if (sh.warp) {
         if (a.rest) launch(distill_kernel<T, 32, true>, sh, s, a);
         else launch(distill_kernel<T, 32, false>, sh, s, a);
