@@ -92,6 +92,16 @@ def _dense(g):
     return g if g is None or g.is_contiguous() else g.contiguous()
 
 
+def _once(backward):
+    """once_differentiable, whose bookkeeping only a backward under create_graph needs."""
+    checked = once_differentiable(backward)
+
+    def run(ctx, *grads):
+        return checked(ctx, *grads) if torch.is_grad_enabled() else backward(ctx, *grads)
+
+    return run
+
+
 class _TokenLogprobsFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, tokens, temperature, top):
@@ -106,7 +116,7 @@ class _TokenLogprobsFn(torch.autograd.Function):
         return lp, h, topv, topi
 
     @staticmethod
-    @once_differentiable
+    @_once
     def backward(ctx, g_lp, g_h, _gv, _gi):
         if g_lp is None and g_h is None:
             return None, None, None, None
@@ -125,7 +135,7 @@ class _TopkDistillationFn(torch.autograd.Function):
         return loss
 
     @staticmethod
-    @once_differentiable
+    @_once
     def backward(ctx, gl):
         logits, ids, values, stats = ctx.saved_tensors
         return (ops._distillation_grad(logits, ctx.rows, ids, values, ctx.temperature, ctx.rest, stats, _dense(gl)),
