@@ -37,6 +37,39 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
+// Two fp32 values in one register pair: one instruction for both.
+__device__ __forceinline__ float2 sub2(float2 a, float b) {
+    float2 r;
+    const float2 m = make_float2(-b, -b);
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(m)));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float b) {
+    float2 r;
+    const float2 m = make_float2(b, b);
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(m)));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
+          "l"(reinterpret_cast<const uint64_t&>(c)));
+    return r;
+}
+
 template <class T>
 struct Elem;
 template <>
@@ -64,6 +97,11 @@ struct Elem<float> {
     }
     __device__ __forceinline__ static void unpack(const uint4& v, float* f) {
         f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+    }
+    __device__ __forceinline__ static void minus(const uint4& v, float m, float* f) {
+        unpack(v, f);
+        const float2 a = sub2(make_float2(f[0], f[1]), m), b = sub2(make_float2(f[2], f[3]), m);
+        f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
     }
 };
 template <>
@@ -101,6 +139,15 @@ struct Elem<__half> {
     __device__ __forceinline__ static void unpack(const uint4& v, float* f) {
         pair(v.x, f), pair(v.y, f + 2), pair(v.z, f + 4), pair(v.w, f + 6);
     }
+    // x - m in fp32, straight from the two halves of a word
+    __device__ __forceinline__ static void minus(const uint4& v, float m, float* f) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n sub.rn.f32.f16 %0, lo, %3;\n sub.rn.f32.f16 %1, hi, %3;\n}"
+                : "=f"(f[2 * i]), "=f"(f[2 * i + 1])
+                : "r"(w[i]), "f"(m));
+    }
 };
 template <>
 struct Elem<__nv_bfloat16> {
@@ -135,6 +182,15 @@ struct Elem<__nv_bfloat16> {
     }
     __device__ __forceinline__ static void unpack(const uint4& v, float* f) {
         pair(v.x, f), pair(v.y, f + 2), pair(v.z, f + 4), pair(v.w, f + 6);
+    }
+    // x - m in fp32, straight from the two halves of a word
+    __device__ __forceinline__ static void minus(const uint4& v, float m, float* f) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n sub.rn.f32.bf16 %0, lo, %3;\n sub.rn.f32.bf16 %1, hi, %3;\n}"
+                : "=f"(f[2 * i]), "=f"(f[2 * i + 1])
+                : "r"(w[i]), "f"(m));
     }
 };
 
@@ -299,39 +355,6 @@ struct State {
     }
 };
 
-// Two fp32 values in one register pair: one instruction for both.
-__device__ __forceinline__ float2 sub2(float2 a, float b) {
-    float2 r;
-    const float2 m = make_float2(-b, -b);
-    asm("add.rn.f32x2 %0, %1, %2;"
-        : "=l"(reinterpret_cast<uint64_t&>(r))
-        : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(m)));
-    return r;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float b) {
-    float2 r;
-    const float2 m = make_float2(b, b);
-    asm("mul.rn.f32x2 %0, %1, %2;"
-        : "=l"(reinterpret_cast<uint64_t&>(r))
-        : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(m)));
-    return r;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 r;
-    asm("add.rn.f32x2 %0, %1, %2;"
-        : "=l"(reinterpret_cast<uint64_t&>(r))
-        : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
-    return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(reinterpret_cast<uint64_t&>(r))
-        : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
-          "l"(reinterpret_cast<const uint64_t&>(c)));
-    return r;
-}
-
 // N vectors of scores into the state. For two scores: unpacking two, half a maximum each, x - m, the product
 // with c, two ex2 and the sum s. MOMENT: h too; a masked score's distance (-inf) is bounded, as its weight 0 times
 // it would be NaN. Without h, the product is formed with both words of c instead (c_lo > 0, so that -inf stays).
@@ -347,11 +370,11 @@ __device__ __forceinline__ float add_scores(State& st, const uint4 (&r)[N], cons
 #pragma unroll
     for (int u = 0; u < N; ++u) {
         float f[V];
-        Elem<T>::unpack(r[u], f);
+        Elem<T>::minus(r[u], top, f);
 #pragma unroll
         for (int i = 0; i < V; i += 2) {
             const int k = i / 2 & 1;
-            float2 d = sub2(make_float2(f[i], f[i + 1]), top), x;
+            float2 d = make_float2(f[i], f[i + 1]), x;
             if (MOMENT) {
                 d = make_float2(max_nan(d.x, -1e30f), max_nan(d.y, -1e30f));
                 x = mul2(d, sc.c);
