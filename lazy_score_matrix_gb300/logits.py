@@ -84,8 +84,9 @@ def topk_distillation_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teac
     return loss, grad
 
 
-# The forwards keep what their backwards need in the form that the C entry takes: a backward runs on autograd's own
-# thread, where every step costs twice what it does on the caller's.
+# The backwards run on autograd's own thread, where a step costs twice what it does on the caller's: what the forward
+# has checked is not checked again. Pointers are taken anew: a saved tensor may come back at another address (hooks
+# that move saved tensors to the host and back).
 
 
 def _dense(g):
@@ -105,7 +106,7 @@ def _once(backward):
 class _TokenLogprobsFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, tokens, temperature, top):
-        ctx.rows, kept = ops._rows(logits)
+        kept = ops._rows(logits)[1]
         tokens = ops._side(tokens, torch.int64, "tokens", logits.shape[:-1], logits)
         lp, h, topv, topi, stats = ops.token_logprobs(kept, tokens, temperature, top, want_stats=True)
         ctx.set_materialize_grads(False)
@@ -121,14 +122,15 @@ class _TokenLogprobsFn(torch.autograd.Function):
         if g_lp is None and g_h is None:
             return None, None, None, None
         logits, tokens, stats = ctx.saved_tensors
-        return ops._logprobs_grad(logits, ctx.rows, tokens, ctx.temperature, stats, _dense(g_lp), _dense(g_h)), None, None, None
+        r, logits = ops._rows(logits)
+        return ops._logprobs_grad(logits, r, tokens, ctx.temperature, stats, _dense(g_lp), _dense(g_h)), None, None, None
 
 
 class _TopkDistillationFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, ids, values, temperature, rest):
-        ctx.rows, kept = ops._rows(logits)
-        _, ids, values = ops._teacher(kept, ctx.rows, ids, values)
+        r, kept = ops._rows(logits)
+        _, ids, values = ops._teacher(kept, r, ids, values)
         loss, stats = ops.topk_distillation(kept, ids, values, temperature, rest, want_stats=True)
         ctx.save_for_backward(kept, ids, values, stats)
         ctx.temperature, ctx.rest = temperature, rest
@@ -138,5 +140,6 @@ class _TopkDistillationFn(torch.autograd.Function):
     @_once
     def backward(ctx, gl):
         logits, ids, values, stats = ctx.saved_tensors
-        return (ops._distillation_grad(logits, ctx.rows, ids, values, ctx.temperature, ctx.rest, stats, _dense(gl)),
+        r, logits = ops._rows(logits)
+        return (ops._distillation_grad(logits, r, ids, values, ctx.temperature, ctx.rest, stats, _dense(gl)),
                 None, None, None, None)

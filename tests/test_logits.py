@@ -145,6 +145,140 @@ def test_long_rows_and_many_elements(dtype):
     assert ((grad.double() - want).abs() <= tol).all()
 
 
+# The kernels' shapes: a warp a row, a CTA a row, a cluster a row, one CTA alone on an SM; every one with rows at odd
+# addresses, some left out, masked columns, and lists that lie across the parts of a long row. Checked whole against
+# fp64 torch, with _rows_ref.py's bounds formed for all rows at once.
+SHAPES = [(1300, 261, torch.float32), (1300, 4099, torch.bfloat16), (1216, 8001, torch.float32), (650, 9001, torch.float32),
+          (610, 100003, torch.bfloat16), (300, 32003, torch.float32), (40, 70001, torch.float16), (5, 150001, torch.bfloat16),
+          (2, 300007, torch.bfloat16), (160, 100003, torch.float32), (620, 300007, torch.float16)]
+
+
+def _bounds(x, T):
+    """fp64 rows: d = (x - max)/T, p, log p, l, a, E d^2, and the bound of l."""
+    d = (x - x.amax(1, keepdim=True)) / T
+    l = d.exp().sum(1, keepdim=True).log()
+    p = (d - l).exp()
+    dd = torch.where(p > 0, d, 0.0)
+    a, a2 = -(p * dd).sum(1, keepdim=True), (p * dd * dd).sum(1, keepdim=True)
+    return d, p, d - l, l, a, a2, ref.U * (13 + 2 * a + 3 * l)
+
+
+def _device_scores(n, m, dtype, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x = torch.randn(n, m, device=DEV, generator=g) * 3
+    x.scatter_(1, torch.randint(0, m, (n, 3), device=DEV, generator=g), torch.randn(n, 3, device=DEV, generator=g) + 9)
+    x[:, torch.rand(m, device=DEV, generator=g) < 0.1] = NEG
+    return x.to(dtype)
+
+
+@pytest.mark.parametrize("n,m,dtype", SHAPES)
+def test_logprobs_shapes(n, m, dtype):
+    T, U = 0.9, ref.U
+    x = _device_scores(n, m, dtype, n + m)
+    i = torch.arange(n, device=DEV)
+    tok = (i * 7919) % m
+    tok[3::11] = -1
+    kept = tok >= 0
+    g1, g2 = torch.linspace(-1, 1, n, device=DEV), torch.linspace(0.2, -0.3, n, device=DEV)
+    for top in (20, 100):
+        leaf = x.detach().requires_grad_(top == 20)
+        r = tp.token_logprobs(leaf, tok, temperature=T, top=top)
+        x64 = x.double()
+        d, p, logp, l, a, a2, l_tol = _bounds(x64, T)
+        t = tok.clamp(min=0)[:, None]
+        lp, dt = logp.gather(1, t)[:, 0], d.gather(1, t)[:, 0]
+        fin = kept & (lp > NEG)
+        assert (r.logprobs[~kept] == 0).all() and (r.logprobs[kept & (lp == NEG)] == NEG).all()
+        tol = 2 * (l_tol[:, 0] + U * (3 * dt.abs() + lp.abs())) + U * lp.abs()
+        assert ((r.logprobs.double() - lp).abs() <= tol)[fin].all()
+        h = -torch.where(p > 0, p * logp, 0.0).sum(1, keepdim=True)
+        h_tol = 2 * (l_tol + U * (16 * a + 2 * a2 + h)) + U * h
+        assert ((r.entropy.double() - h[:, 0]).abs() <= h_tol[:, 0])[kept].all() and (r.entropy[~kept] == 0).all()
+        order = torch.sort(x.float(), dim=1, descending=True, stable=True).indices[:, :top]
+        assert torch.equal(r.top_ids[kept], order[kept]) and (r.top_ids[~kept] == -1).all()
+        v, dv = logp.gather(1, order), d.gather(1, order)
+        assert ((r.top_logprobs.double() - v).abs() <= 2 * (l_tol + U * (3 * dv.abs() + v.abs())) + U * v.abs())[kept].all()
+        if top == 20:
+            grad, = torch.autograd.grad((r.logprobs, r.entropy), leaf, (g1, g2))
+            w1, w2 = (torch.where(kept, w, 0.0).double()[:, None] for w in (g1, g2))
+            lf = torch.where(p > 0, logp, 0.0)
+            want = -p * (w1 + w2 * (lf + h))
+            want[i, t[:, 0]] += w1[:, 0]
+            want /= T
+            dc = d.clamp(min=-200.0).abs()
+            mag = w1.abs() + w2.abs() * (lf.abs() + h)
+            tol = 2 * ((p + ref.FLUSH) * mag * (l_tol + U * (4 * (dc + l) + 10)) + p * w2.abs() * (h_tol + l_tol + 4 * U * (dc + l)) + 4 * U * w1.abs()) / T
+            assert ((grad.double() - want).abs() <= tol + ref.STEP[dtype] * 1.001 * want.abs() + ref.TINY[dtype]).all()
+            del grad, want, mag, tol, lf, dc
+        del x64, d, p, logp, order
+
+
+@pytest.mark.parametrize("n,m,dtype", SHAPES)
+@pytest.mark.parametrize("rest", [False, True])
+def test_distill_shapes(n, m, dtype, rest):
+    T, K, U = 1.2, 50, ref.U
+    x = _device_scores(n, m, dtype, n * 3 + m)
+    g = torch.Generator(device=DEV).manual_seed(7)
+    y = torch.where(x > NEG, x.float(), -40.0) + 0.7 * T * torch.randn(n, m, device=DEV, generator=g)
+    if rest:
+        y = torch.log_softmax(y.double() / T, 1).float()
+    values, ids = y.topk(K, 1)
+    if rest:
+        values = values - 0.3  # a share for the others everywhere
+    del y
+    ids[2::9, K // 2:] = -1
+    ids[5::13] = -1
+    values[7::10, 3] = NEG
+    w = torch.rand(n, device=DEV, generator=g) + 0.5
+    leaf = x.detach().requires_grad_(True)
+    loss = tp.topk_distillation(leaf, ids, values, temperature=T, rest=rest)
+    grad, = torch.autograd.grad(loss, leaf, w)
+    loss2, grad2 = tp.topk_distillation_grad(x, ids, values, w, temperature=T, rest=rest)
+    inplace = x.clone()
+    loss3, _ = tp.topk_distillation_grad(inplace, ids, values, w, temperature=T, rest=rest, out=inplace)
+    assert torch.equal(loss2, loss3) and torch.equal(grad2, inplace)
+    del inplace
+    d, p, logp, l, a, _, l_tol = _bounds(x.double(), T)
+    ok = (ids >= 0) & (values > NEG)
+    kept = ok.any(1, keepdim=True)
+    at = ids.clamp(min=0)
+    logq = torch.where(ok, values.double() if rest else values.double() / T, NEG)
+    if not rest:
+        logq = logq - torch.logsumexp(logq, 1, keepdim=True).clamp(min=-1e300)
+    q = torch.where(ok, logq.exp(), 0.0)
+    want = (torch.where(q > 0, q * (logq - logp.gather(1, at)), 0.0)).sum(1, keepdim=True)
+    Z = q.sum(1, keepdim=True)
+    listed = torch.zeros(n, m + 1, dtype=torch.bool, device=DEV).scatter_(1, torch.where(ok, at, m), True)[:, :m]
+    share = torch.zeros(n, m, dtype=torch.float64, device=DEV).scatter_add_(1, at, q)
+    dc = d.clamp(min=-200.0).abs()
+    if rest:
+        other = torch.where(listed, NEG, x.double())
+        dr, r, _, lr, ar, _, lr_tol = _bounds(other, T)
+        gap = ((other.amax(1, keepdim=True) - x.double().amax(1, keepdim=True)) / T)
+        log_pr = gap + lr - l
+        q_r = torch.where(kept & (1 - Z >= 2.0 ** -20), 1 - Z, 0.0)
+        want = want + torch.where(q_r > 0, q_r * (q_r.clamp(min=1e-300).log() - log_pr), 0.0)
+        Z = Z + q_r
+        p_r = log_pr.exp()
+        gen = torch.where(listed, p * Z, (Z * p_r - q_r) * r)
+        coef_tol = Z * p_r * (l_tol + lr_tol + U * (4 * gap.abs() + 4 * l + 4 * lr + 8)) + 8 * U * (K ** 0.5 + 1)
+        gen_tol = torch.where(listed, p * Z * (l_tol + U * (4 * (dc + l) + 8)),
+                              r * (coef_tol + (Z * p_r - q_r).abs() * (lr_tol + U * (4 * (dr.clamp(min=-200.0).abs() + lr) + 8))))
+        loss_tol = 2 * (Z * (l_tol + lr_tol) + U * want.abs() + 1e-13) + U * want.abs()
+        del other, dr, r
+    else:
+        gen, gen_tol = p * Z, p * Z * (l_tol + U * (4 * (dc + l) + 8))
+        loss_tol = 2 * (Z * l_tol + U * want.abs() + 1e-13) + U * want.abs()
+    want = torch.where(kept, want, 0.0)[:, 0]
+    spread = torch.where(q > 0, logq.abs(), 0.0).amax(1, keepdim=True).clamp(max=200.0)
+    wg = torch.where(kept[:, 0], w, 0.0).double()[:, None]
+    gw = wg * (gen - share) / T
+    tol = 2 * (wg / T) * (ref.FLUSH + gen_tol + share * U * (12 + 6 * spread)) + 2 * U * gw.abs() + ref.STEP[dtype] * 1.001 * gw.abs() + ref.TINY[dtype]
+    for name, lo, gr in (("autograd", loss.detach(), grad), ("at once", loss2, grad2)):
+        assert ((lo.double() - want).abs() <= loss_tol[:, 0])[kept[:, 0]].all() and (lo[~kept[:, 0]] == 0).all(), name
+        assert ((gr.double() - gw).abs() <= tol).all(), name
+
+
 # --- masks, ties, orders ------------------------------------------------------------------------------------------
 
 
@@ -423,6 +557,31 @@ def test_in_place_and_given_output():
     with pytest.raises(RuntimeError):  # the graph of `kept` needs the overwritten scores
         kept.logprobs.sum().backward()
     hold.logprobs.sum().backward()
+
+
+def test_saved_tensors_that_move():
+    # hooks that bring saved tensors back at another address
+    x = scores(4, 700, torch.float32, 3).to(DEV)
+    ids, values = (t.to(DEV) for t in teacher_list(x.cpu(), 6, 1.0, False, 3))
+
+    def grads(view):
+        leaf = x.detach().requires_grad_(True)
+        y = view(leaf)
+        r = tp.token_logprobs(y, ids[:, 0])
+        return torch.autograd.grad(r.logprobs.sum() + r.entropy.sum() + tp.topk_distillation(y, ids, values).sum(), leaf)[0]
+
+    for view in (lambda t: t, lambda t: torch.cat([t, t], 1)[:, :700], lambda t: t.t().contiguous().t()):
+        want = grads(view)
+        with torch.autograd.graph.save_on_cpu():
+            got = grads(view)
+        assert torch.equal(got, want)
+
+
+def test_leading_shapes_that_need_a_copy():
+    x = scores(2 * 3 * 4, 90, torch.bfloat16, 4).to(DEV).view(2, 3, 4, 90)[:, :2, :3]
+    r, want = tp.token_logprobs(x, top=3), tp.token_logprobs(x.reshape(-1, 90), top=3)
+    assert r.top_ids.shape == (2, 2, 3, 3) and torch.equal(r.top_ids.reshape(-1, 3), want.top_ids)
+    assert torch.equal(r.entropy.reshape(-1), want.entropy)
 
 
 def test_integer_types_and_teacher_types():

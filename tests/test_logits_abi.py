@@ -175,3 +175,39 @@ def test_plain_forms_agree_with_autograd(seed):
     want, = torch.autograd.grad(loss, x)
     d = ref.distill(x.detach(), ids.tolist(), y.tolist(), T, True)
     assert abs(d["loss"] - float(loss.detach())) < 1e-12 and (d["grad"] - want).abs().max() < 1e-12
+
+
+def test_two_word_tables_are_right():
+    """The tables of csrc_logits/tp_logits_two.cuh, recomputed in 60-digit decimal arithmetic: 2^(j/32) and -ln c as
+    the nearest float and the nearest float to what is left, c the multiple of 2^-9 nearest to 1/(1 + (i + 1/2)/32);
+    the words of ln 2 and ln2/32 sum to them."""
+    import os
+    import re
+    import struct
+    from decimal import Decimal, getcontext
+    getcontext().prec = 60
+    src = open(os.path.join(_lib.PKG, "csrc_logits", "tp_logits_two.cuh")).read()
+    number = r"-?0x[0-9a-f.]+p[+-]\d+|0\.f|0x0\.0p[+-]\d+"
+
+    def table(name):
+        body = src[src.index(name):]
+        body = body[body.index("= {") + 3:body.index("};")]
+        return [[float.fromhex(v.rstrip("f")) if "x" in v else 0.0 for v in re.findall(number, row)] for row in re.findall(r"\{([^{}]*)\}", body)]
+
+    f32 = lambda v: struct.unpack("f", struct.pack("f", float(v)))[0]  # noqa: E731
+    ln2 = Decimal(2).ln()
+    exps, lns = table("kExpTab[32]"), table("kLnTab[32]")
+    assert len(exps) == len(lns) == 32
+    for j, (h, lo) in enumerate(exps):
+        want = Decimal(2) ** (Decimal(j) / 32)
+        assert h == f32(want) and lo == f32(want - Decimal(h)), j
+    for i, (c, h, lo) in enumerate(r[:3] for r in lns):
+        mid = 1 + (Decimal(i) + Decimal("0.5")) / 32
+        assert Decimal(c) * 512 == (512 / mid).to_integral_value() and abs(Decimal(c) * mid - 1) < Decimal(1) / 500, i
+        want = -Decimal(c).ln()
+        assert h == f32(want) and lo == f32(want - Decimal(h)), i
+    words = lambda names: [Decimal(float.fromhex(re.search(n + r" = (" + number + ")", src).group(1).rstrip("f"))) for n in names]  # noqa: E731
+    l1, l2, l3 = words(["kL1", "kL2", "kL3"])
+    assert abs(l1 + l2 + l3 - ln2 / 32) < Decimal(2) ** -52 and l1 * 2 ** 17 % 1 == 0 and l2 * 2 ** 28 % 1 == 0
+    hi, lo = words(["kLn2Hi", "kLn2Lo"])
+    assert abs(hi + lo - ln2) < Decimal(2) ** -38 and hi * 2 ** 14 % 1 == 0
