@@ -80,7 +80,7 @@ SIGNATURES = {
     "tp_selftest_exp64": ([_P, _P, _I64, _P], _INT),
 }
 
-# include/tp_logits.h: consumers of stored score rows
+# include/tp_logits.h: consumers of stored score rows (called through logits_binding, but for tests of the C entries)
 LOGITS_SIGNATURES = {
     "tp_token_logprobs": ([_ROWS, _P, _F64, _INT, _P, _P, _P, _P, _P, _P], _INT),
     "tp_token_logprobs_backward": ([_ROWS, _P, _F64, _P, _P, _P, _ROWS, _P], _INT),
@@ -93,7 +93,7 @@ LAUNCH_HOOK = ctypes.CFUNCTYPE(None, ctypes.c_char_p, ctypes.c_int, ctypes.c_voi
 
 _lock = threading.Lock()
 _lib = None
-_logits_lib = None
+_logits_binding = None
 
 
 class TPError(RuntimeError):
@@ -128,20 +128,18 @@ def load(path: str | None = None):
         return lib
 
 
-def load_logits():
-    """The entries of include/tp_logits.h, called with the interpreter lock held: a call only validates and enqueues
-    (a few microseconds), and handing the lock over around it costs more than that inside an autograd backward,
-    which runs on a thread of its own."""
-    global _logits_lib
-    if _logits_lib is None:
+def logits_binding():
+    """The PyTorch binding of include/tp_logits.h (csrc_logits/tp_logits_torch.cpp)."""
+    global _logits_binding
+    if _logits_binding is None:
         load()
-        lib = ctypes.PyDLL(LIB_PATH)
-        for name, (args, res) in LOGITS_SIGNATURES.items():
-            f = getattr(lib, name)
-            f.argtypes = args
-            f.restype = res
-        _logits_lib = lib
-    return _logits_lib
+        try:
+            from . import _tp_logits
+        except ImportError as e:
+            raise ImportError(f"_tp_logits is not built ({e}): run `python -m lazy_score_matrix_gb300.build` or "
+                              "__graft_entry__.build()") from e
+        _logits_binding = _tp_logits
+    return _logits_binding
 
 
 def status_text(status: int) -> str:

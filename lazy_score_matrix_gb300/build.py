@@ -1,4 +1,5 @@
-"""Build libtp.so in-tree: every csrc/*.cu and csrc_logits/*.cu compiled for sm_103a in parallel, then linked.
+"""Build libtp.so in-tree: every csrc/*.cu and csrc_logits/*.cu compiled for sm_103a in parallel, then linked; and
+_tp_logits.so, the PyTorch binding of include/tp_logits.h (csrc_logits/tp_logits_torch.cpp), against it.
 
 Usage: ``python -m lazy_score_matrix_gb300.build`` (or ``__graft_entry__.build()``).
 Objects go to ``lazy_score_matrix_gb300/_build/``; the library to ``lazy_score_matrix_gb300/libtp.so``.
@@ -24,6 +25,8 @@ CSRC_LOGITS = os.path.join(PKG, "csrc_logits")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtp.so")
+BINDING_SRC = os.path.join(CSRC_LOGITS, "tp_logits_torch.cpp")
+BINDING = os.path.join(PKG, "_tp_logits.so")
 # calibration library of the benchmark (measured fp32 / fp64 FMA and exp2 rates), not part of libtp
 PEAKS_SRC = os.path.join(PKG, "peaks", "tp_peaks.cu")
 PEAKS_LIB = os.path.join(PKG, "libtp_peaks.so")
@@ -52,6 +55,36 @@ def _compile(src: str, extra: list[str]) -> tuple[str, int, str]:
     return obj, r.returncode, (r.stdout + r.stderr)
 
 
+def _torch_dirs() -> tuple[list[str], str]:
+    """PyTorch's include directories (with Python's and CUDA's) and its library directory, without importing it."""
+    import importlib.util
+    import sysconfig
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    inc = os.path.join(torch, "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    return [inc, os.path.join(inc, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"], cuda], os.path.join(torch, "lib")
+
+
+def _compile_binding() -> tuple[str, int, str]:
+    obj = os.path.join(OBJ_DIR, "tp_logits_torch.o")
+    incs, _ = _torch_dirs()
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden", "-DTORCH_API_INCLUDE_EXTENSION_H",
+           "-I" + INCLUDE, *[a for d in incs for a in ("-isystem", d)], "-c", BINDING_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    return obj, r.returncode, (r.stdout + r.stderr)
+
+
+def _link_binding() -> None:
+    tmp = BINDING + f".tmp{os.getpid()}"
+    lib = _torch_dirs()[1]
+    r = subprocess.run(["g++", "-shared", "-o", tmp, os.path.join(OBJ_DIR, "tp_logits_torch.o"), "-L" + PKG, "-l:libtp.so",
+                        "-Wl,-rpath,$ORIGIN", "-L" + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10"], capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("_tp_logits link failed")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, jobs: int | None = None, verbose: bool = False, extra: list[str] | None = None) -> str:
     os.makedirs(OBJ_DIR, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu"))) + sorted(glob.glob(os.path.join(CSRC_LOGITS, "*.cu")))
@@ -61,11 +94,15 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False, e
         obj = os.path.join(OBJ_DIR, os.path.basename(s)[:-3] + ".o")
         if force or not os.path.exists(obj) or os.path.getmtime(obj) < max(os.path.getmtime(s), hdr):
             todo.append(s)
-    jobs = jobs or max(1, min(len(todo) or 1, os.cpu_count() or 4))
+    bound = os.path.join(OBJ_DIR, "tp_logits_torch.o")
+    bind = force or not os.path.exists(bound) or os.path.getmtime(bound) < max(
+        os.path.getmtime(BINDING_SRC), *(os.path.getmtime(h) for h in glob.glob(os.path.join(INCLUDE, "*.h"))))
+    jobs = jobs or max(1, min(len(todo) + bind or 1, os.cpu_count() or 4))
     errors = []
-    if todo:
+    if todo or bind:
         with cf.ThreadPoolExecutor(jobs) as ex:
-            for obj, rc, out in ex.map(lambda s: _compile(s, extra or []), todo):
+            work = ([_compile_binding] if bind else []) + [lambda s=s: _compile(s, extra or []) for s in todo]
+            for obj, rc, out in ex.map(lambda f: f(), work):
                 if rc != 0:
                     errors.append((obj, out))
                 elif verbose and out.strip():
@@ -90,6 +127,8 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False, e
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("libtp link failed")
         os.replace(tmp, LIB)
+    if bind or not os.path.exists(BINDING) or os.path.getmtime(BINDING) < os.path.getmtime(bound):
+        _link_binding()
     return LIB
 
 

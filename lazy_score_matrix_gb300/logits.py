@@ -23,9 +23,8 @@ from collections import namedtuple
 from typing import Optional
 
 import torch
-from torch.autograd.function import once_differentiable
 
-from . import ops
+from . import _lib
 
 TokenLogprobs = namedtuple("TokenLogprobs", ["logprobs", "entropy", "top_logprobs", "top_ids"])
 
@@ -41,9 +40,7 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     and gives zeros, (-inf, -1) and a zero gradient. A row of -inf alone has log probability -inf and entropy 0.
 
     Differentiable in logprobs and entropy; the alternatives carry no gradient. temperature in [1e-3, 1e3]."""
-    if torch.is_grad_enabled() and isinstance(logits, torch.Tensor) and logits.requires_grad:
-        return TokenLogprobs(*_TokenLogprobsFn.apply(logits, tokens, float(temperature), int(top)))
-    return TokenLogprobs(*ops.token_logprobs(logits, tokens, float(temperature), int(top))[:4])
+    return TokenLogprobs(*_lib.logits_binding().token_logprobs(logits, tokens, temperature, top))
 
 
 def topk_distillation(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_values: torch.Tensor, *,
@@ -62,84 +59,15 @@ def topk_distillation(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_v
     not read, loss 0, gradient 0. A column listed twice holds both shares. Differentiable in the logits; the
     teacher's list is a constant. Multiply by temperature ** 2 to keep gradients of different temperatures in
     proportion."""
-    if isinstance(teacher_values, torch.Tensor) and teacher_values.requires_grad and torch.is_grad_enabled():
-        raise ValueError("topk_distillation: the teacher's list is a constant; pass teacher_values.detach()")
-    if torch.is_grad_enabled() and isinstance(logits, torch.Tensor) and logits.requires_grad:
-        return _TopkDistillationFn.apply(logits, teacher_ids, teacher_values, float(temperature), bool(rest))
-    return ops.topk_distillation(logits, teacher_ids, teacher_values, float(temperature), rest)[0]
+    return _lib.logits_binding().topk_distillation(logits, teacher_ids, teacher_values, temperature, rest)
 
 
-@torch.no_grad()
 def topk_distillation_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_values: torch.Tensor,
                            weights: Optional[torch.Tensor] = None, *, temperature: float = 1.0, rest: bool = False,
                            out: Optional[torch.Tensor] = None):
     """(loss [...], gradient [..., M] of sum(weights * loss)) in one call, for row weights [...] known beforehand
-    (a mask over the number of tokens, a loss scale; all ones when None). The loss is not weighted. The row is
-    read once for both, so this is the form for training: ``logits.backward(gradient)``.
+    (a mask over the number of tokens, a loss scale; all ones when None). The loss is not weighted. Each row
+    comes from memory once for both, so this is the form for training: ``logits.backward(gradient)``.
 
     out: where the gradient is written; it may be the logits themselves, which are then overwritten."""
-    loss, grad = ops.topk_distillation_grad(logits, teacher_ids, teacher_values, weights, float(temperature), rest, out)
-    if out is not None:
-        torch.autograd.graph.increment_version(out)  # a graph that saved it must not use it any more
-    return loss, grad
-
-
-# The backwards run on autograd's own thread, where a step costs twice what it does on the caller's: what the forward
-# has checked is not checked again. Pointers are taken anew: a saved tensor may come back at another address (hooks
-# that move saved tensors to the host and back).
-
-
-def _dense(g):
-    return g if g is None or g.is_contiguous() else g.contiguous()
-
-
-def _once(backward):
-    """once_differentiable, whose bookkeeping only a backward under create_graph needs."""
-    checked = once_differentiable(backward)
-
-    def run(ctx, *grads):
-        return checked(ctx, *grads) if torch.is_grad_enabled() else backward(ctx, *grads)
-
-    return run
-
-
-class _TokenLogprobsFn(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, logits, tokens, temperature, top):
-        kept = ops._rows(logits)[1]
-        tokens = ops._side(tokens, torch.int64, "tokens", logits.shape[:-1], logits)
-        lp, h, topv, topi, stats = ops.token_logprobs(kept, tokens, temperature, top, want_stats=True)
-        ctx.set_materialize_grads(False)
-        if top:
-            ctx.mark_non_differentiable(topv, topi)
-        ctx.save_for_backward(kept, tokens, stats)
-        ctx.temperature = temperature
-        return lp, h, topv, topi
-
-    @staticmethod
-    @_once
-    def backward(ctx, g_lp, g_h, _gv, _gi):
-        if g_lp is None and g_h is None:
-            return None, None, None, None
-        logits, tokens, stats = ctx.saved_tensors
-        r, logits = ops._rows(logits)
-        return ops._logprobs_grad(logits, r, tokens, ctx.temperature, stats, _dense(g_lp), _dense(g_h)), None, None, None
-
-
-class _TopkDistillationFn(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, logits, ids, values, temperature, rest):
-        r, kept = ops._rows(logits)
-        _, ids, values = ops._teacher(kept, r, ids, values)
-        loss, stats = ops.topk_distillation(kept, ids, values, temperature, rest, want_stats=True)
-        ctx.save_for_backward(kept, ids, values, stats)
-        ctx.temperature, ctx.rest = temperature, rest
-        return loss
-
-    @staticmethod
-    @_once
-    def backward(ctx, gl):
-        logits, ids, values, stats = ctx.saved_tensors
-        r, logits = ops._rows(logits)
-        return (ops._distillation_grad(logits, r, ids, values, ctx.temperature, ctx.rest, stats, _dense(gl)),
-                None, None, None, None)
+    return _lib.logits_binding().topk_distillation_grad(logits, teacher_ids, teacher_values, weights, temperature, rest, out)

@@ -2,8 +2,7 @@
 PyTorch's caching allocator, the current CUDA stream, and the libtp call. Every step of the
 computation runs in libtp's kernels; nothing here computes on the data.
 
-Each function mirrors one C entry point of include/tp.h or include/tp_logits.h (same name without the
-``tp_`` prefix).
+Each function mirrors one C entry point of include/tp.h (same name without the ``tp_`` prefix).
 """
 from __future__ import annotations
 
@@ -286,200 +285,3 @@ def pairwise_topk_backward(X, Y, score: Score, k, indices, grad_values, want=ALL
                                                *_gp(g), *_ws_args(c.workspace("pairwise_topk_backward", 0, k)),
                                                c.stream), "tp_pairwise_topk_backward")
     return g
-
-
-# ------------------------------------------------------------------------------------------------
-# stored score rows (include/tp_logits.h): logits [..., M] read where they lie
-# ------------------------------------------------------------------------------------------------
-
-_ROWS_DT = {torch.float32: _lib.TP_ROWS_F32, torch.float16: _lib.TP_ROWS_F16, torch.bfloat16: _lib.TP_ROWS_BF16}
-STATS = 8  # floats per row that a forward leaves for its backward
-
-
-def _row_strides(t):
-    """(group, row_stride, group_stride) of the rows t[..., :], or None when two strides do not describe them."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        return None
-    dims = []  # leading dimensions with adjacent ones joined where they can be: [size, stride], outermost first
-    for n, st in zip(t.shape[:-1], t.stride()[:-1]):
-        if n == 1:
-            continue
-        if dims and dims[-1][1] == st * n:
-            dims[-1] = [dims[-1][0] * n, st]
-        else:
-            dims.append([n, st])
-    if len(dims) > 2:
-        return None
-    if len(dims) == 2:
-        return dims[1][0], dims[1][1], dims[0][1]
-    return (dims[0][0], dims[0][1], 0) if dims else (1, t.shape[-1], 0)
-
-
-def _rows(t, name="logits", copy=True):
-    """The tp_rows of t [..., M] and the tensor it points into (a contiguous copy where its strides need one)."""
-    kind = _ROWS_DT.get(t.dtype) if isinstance(t, torch.Tensor) else None
-    if kind is None:
-        raise TypeError(f"{name} must be a float32, float16 or bfloat16 tensor, got {getattr(t, 'dtype', type(t).__name__)}")
-    shape = t.shape
-    if not shape or shape[-1] < 1:
-        raise ValueError(f"{name} must have shape [..., M] with M >= 1, got {tuple(shape)}")
-    if not t.is_cuda:
-        raise ValueError("libtp runs on CUDA tensors only (no CPU fallback)")
-    M = shape[-1]
-    if len(shape) == 2:
-        row, one = t.stride()
-        if one == 1 or M == 1:
-            return _lib.tp_rows(kind, shape[0], M, shape[0], row, 0, t.data_ptr()), t
-    strides = _row_strides(t)
-    if strides is None:
-        if not copy:
-            raise ValueError(f"{name}: its rows must be contiguous and lie at one stride, or at two")
-        t = t.contiguous()
-        strides = (t.numel() // M, M, 0)
-    return _lib.tp_rows(kind, t.numel() // M, M, *strides, t.data_ptr()), t
-
-
-def _side(t, dtype, name, shape, like):
-    """A dense per-row array of the call: dtype checked or converted, contiguous, on the logits' device."""
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
-    if t.dtype is not dtype:
-        whole = not (t.dtype.is_floating_point or t.dtype.is_complex or t.dtype == torch.bool)
-        if not (whole if dtype == torch.int64 else t.dtype.is_floating_point):
-            raise TypeError(f"{name} must be {'an integer' if dtype == torch.int64 else 'a floating-point'} tensor, got {t.dtype}")
-        t = t.to(dtype)
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != like.device:
-        raise ValueError("all tensors must be on the same device")
-    return t.contiguous()
-
-
-def _p(t):
-    return None if t is None else t.data_ptr()
-
-
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
-
-
-def _launch(entry, device, *args):
-    """One call of a tp_logits.h entry on the device's current stream."""
-    call = getattr(_lib.load_logits(), entry)
-    i = device.index
-    if i == torch.cuda.current_device():
-        status = call(*args, _raw_stream(i))
-    else:
-        with torch.cuda.device(device):
-            status = call(*args, _raw_stream(i))
-    if status != _lib.TP_OK:
-        _lib.check(status, entry)
-
-
-def token_logprobs(logits, tokens, temperature: float = 1.0, top: int = 0, want_stats: bool = False):
-    """(logprobs | None, entropy, top_logprobs | None, top_ids | None, stats | None) of logits [..., M]."""
-    r, logits = _rows(logits)
-    lead, dev = logits.shape[:-1], logits.device
-    tokens = _side(tokens, torch.int64, "tokens", lead, logits)
-    if top < 0 or top > 128 or top > r.M:
-        raise ValueError(f"top must be in [0, min(M, 128)], got {top}")
-    entropy = torch.empty(lead, dtype=torch.float32, device=dev)
-    logprobs = topv = topi = stats = None
-    if tokens is not None:
-        logprobs = torch.empty(lead, dtype=torch.float32, device=dev)
-    if top:
-        topv = torch.empty((*lead, top), dtype=torch.float32, device=dev)
-        topi = torch.empty((*lead, top), dtype=torch.int64, device=dev)
-    if want_stats:
-        stats = torch.empty((r.N, STATS), dtype=torch.float32, device=dev)
-    if r.N:
-        _launch("tp_token_logprobs", dev, r, _p(tokens), temperature, top, _p(logprobs), entropy.data_ptr(), _p(stats),
-                _p(topv), _p(topi))
-    return logprobs, entropy, topv, topi, stats
-
-
-def token_logprobs_backward(logits, tokens, temperature, stats, grad_logprobs, grad_entropy):
-    r, logits = _rows(logits)
-    lead = logits.shape[:-1]
-    tokens = _side(tokens, torch.int64, "tokens", lead, logits)
-    stats = _side(stats, torch.float32, "stats", (r.N, STATS), logits)
-    g1 = _side(grad_logprobs, torch.float32, "grad_logprobs", lead, logits)
-    g2 = _side(grad_entropy, torch.float32, "grad_entropy", lead, logits)
-    return _logprobs_grad(logits, r, tokens, temperature, stats, g1, g2)
-
-
-def _logprobs_grad(logits, r, tokens, temperature, stats, g1, g2):
-    """The gradient from arguments that are known to be in order (what autograd kept of the forward)."""
-    grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-    if r.N:
-        _launch("tp_token_logprobs_backward", logits.device, r, _p(tokens), temperature, stats.data_ptr(), _p(g1), _p(g2),
-                _dense(r, grad))
-    return grad
-
-
-def _dense(r, t):
-    """The tp_rows of a contiguous tensor of the shape and type of r's."""
-    return _lib.tp_rows(r.dtype, r.N, r.M, r.N, r.M, 0, t.data_ptr())
-
-
-def _teacher(logits, r, ids, values):
-    if not isinstance(ids, torch.Tensor) or ids.dim() < 1:
-        raise TypeError("teacher_ids must be an integer tensor [..., K]")
-    K = ids.shape[-1]
-    if not 1 <= K <= 128:
-        raise ValueError(f"a teacher's list has 1 to 128 columns a row, got {K}")
-    shape = (*logits.shape[:-1], K)
-    return (K, _side(ids, torch.int64, "teacher_ids", shape, logits),
-            _side(values, torch.float32, "teacher_values", shape, logits))
-
-
-def topk_distillation(logits, teacher_ids, teacher_values, temperature: float = 1.0, rest: bool = False,
-                      want_stats: bool = False):
-    r, logits = _rows(logits)
-    K, ids, values = _teacher(logits, r, teacher_ids, teacher_values)
-    loss = torch.empty(logits.shape[:-1], dtype=torch.float32, device=logits.device)
-    stats = torch.empty((r.N, STATS), dtype=torch.float32, device=logits.device) if want_stats else None
-    if r.N:
-        _launch("tp_topk_distillation", logits.device, r, K, ids.data_ptr(), values.data_ptr(), temperature, bool(rest),
-                loss.data_ptr(), _p(stats))
-    return loss, stats
-
-
-def topk_distillation_backward(logits, teacher_ids, teacher_values, temperature, rest, stats, grad_loss):
-    r, logits = _rows(logits)
-    K, ids, values = _teacher(logits, r, teacher_ids, teacher_values)
-    stats = _side(stats, torch.float32, "stats", (r.N, STATS), logits)
-    gl = _side(grad_loss, torch.float32, "grad_loss", logits.shape[:-1], logits)
-    return _distillation_grad(logits, r, ids, values, temperature, rest, stats, gl)
-
-
-def _distillation_grad(logits, r, ids, values, temperature, rest, stats, gl):
-    """The gradient from arguments that are known to be in order (what autograd kept of the forward)."""
-    grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-    if r.N:
-        _launch("tp_topk_distillation_backward", logits.device, r, ids.shape[-1], ids.data_ptr(), values.data_ptr(),
-                temperature, bool(rest), stats.data_ptr(), gl.data_ptr(), _dense(r, grad))
-    return grad
-
-
-def topk_distillation_grad(logits, teacher_ids, teacher_values, weights=None, temperature: float = 1.0,
-                           rest: bool = False, out=None):
-    given = logits
-    r, logits = _rows(logits)
-    K, ids, values = _teacher(logits, r, teacher_ids, teacher_values)
-    dev = logits.device
-    weights = _side(weights, torch.float32, "weights", logits.shape[:-1], logits)
-    if out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
-        g = _dense(r, out)
-    else:
-        if out.shape != given.shape or out.dtype != given.dtype or out.device != given.device:
-            raise ValueError("out must have the logits' shape, dtype and device")
-        g = _rows(out, "out", copy=False)[0]
-    loss = torch.empty(logits.shape[:-1], dtype=torch.float32, device=dev)
-    stats = torch.empty((r.N, STATS), dtype=torch.float32, device=dev)
-    if r.N:
-        _launch("tp_topk_distillation_grad", dev, r, K, ids.data_ptr(), values.data_ptr(), _p(weights), temperature,
-                bool(rest), loss.data_ptr(), stats.data_ptr(), g)
-    return loss, out

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import lazy_score_matrix_gb300 as tp
-from lazy_score_matrix_gb300 import _lib, ops
+from lazy_score_matrix_gb300 import _lib
 from tests import _rows_ref as ref
 
 pytestmark = pytest.mark.gpu
@@ -427,7 +427,7 @@ def test_batches_and_shifted_views():
                                                                       (x[:, :-1], x[:, 1:], x.transpose(0, 1), x[:, ::2])].index(True)]
         for f in ("logprobs", "entropy", "top_logprobs", "top_ids"):
             assert same(getattr(r, f), getattr(whole, f)[at]), f
-        assert ops._rows(view)[1] is view  # read where it lies
+        assert _lib.logits_binding().row_strides(view) is not None  # read where it lies
     leaf = x.detach().requires_grad_(True)
     tp.token_logprobs(leaf[:, :-1], tok[:, :-1]).logprobs.sum().backward()
     flat = x.reshape(-1, m).detach().requires_grad_(True)
@@ -655,7 +655,7 @@ def test_outputs_stay_inside_their_buffers():
     ids, values = (t.to(DEV) for t in teacher_list(x.cpu(), k, 1.0, True, 3))
     tok = torch.arange(n, device=DEV)
     lib = _lib.load()
-    rows = ops._rows(x)[0]
+    rows = _lib.tp_rows(_lib.TP_ROWS_BF16, n, m, n, m, 0, x.data_ptr())
     stream = torch.cuda.current_stream().cuda_stream
 
     def buf(count, dtype):
