@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_bwd_kernel(const LogprobArg
     const float b1 = fmaf(g2, H, g1), b2 = g2 * kLn2;
     const Source<T> x = from_row<T>(row_at<const T>(a.x, row), a.x.M, o);
     Fetch<T, TEAM, true> scores(o, r.e0, r.e1, x);
-    map_range<T, TEAM, true>(o, r.e0, r.e1, scores, [&](float* f, int e) {
+    map_range<T, TEAM>(o, r.e0, r.e1, scores, [&](float* f, int e) {
 #pragma unroll
         for (int i = 0; i < Elem<T>::kVec; ++i) {
             float t = fmaf(f[i] - m, c, -ls2);  // log2 p
@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_bwd_kernel(const LogprobArg
 }
 
 template <class T, int TEAM>
-__global__ void __launch_bounds__(kThreads) distill_bwd_kernel(const DistillArgs a, int parts) {
+__global__ void __launch_bounds__(kThreads, 4) distill_bwd_kernel(const DistillArgs a, int parts) {
     using Tm = Team<TEAM>;
     __shared__ ListBuf lists[Tm::kPerCta];
     const int64_t row = row_of<TEAM>(a.N, parts);
@@ -62,14 +62,14 @@ __global__ void __launch_bounds__(kThreads) distill_bwd_kernel(const DistillArgs
     const float* st = a.stats + row * kStats;
     if (!load_list<TEAM>(a, row, list) || st[0] == neg_inf()) return zero_range<T, TEAM>(o, r.e0, r.e1);
     const Source<T> from = from_row<T>(p, a.x.M, o);
-    Fetch<T, TEAM, true> scores(o, r.e0, r.e1, from);
+    Fetch<T, TEAM, true, true> scores(o, r.e0, r.e1, from);
     const bool twice = look_up<T, TEAM>(a, p, list, r.e0, r.e1);
     if (TEAM == 32 || threadIdx.x < 32) shares(a, list);
     Tm::sync();
     RowStats s;
     s.m = st[0], s.ls = st[1], s.gm = st[2], s.gls = st[3], s.Z = st[4], s.coef = st[5];
     const float w = (a.weights ? a.weights[row] : 1.f) * a.sc.inv;
-    distill_row_grad<T, TEAM, true>(a, s, w, o, r.e0, r.e1, scores);
+    distill_row_grad<T, TEAM>(a, s, w, o, r.e0, r.e1, scores);
     Tm::sync();
     distill_list_grad<T, TEAM>(a, s, w, o, r.e0, r.e1, list, twice);
 }

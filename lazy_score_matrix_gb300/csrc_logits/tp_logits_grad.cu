@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(TEAM == 32 ? kThreads : TEAM, TEAM == kLongThr
     }
     if (s.m == neg_inf()) return zero_range<T, TEAM>(o, e0, e1);  // a row of -inf alone
     const float w = (a.weights ? a.weights[row] : 1.f) * a.sc.inv;
-    distill_row_grad<T, TEAM, true>(a, s, w, o, e0, e1, scores);
+    distill_row_grad<T, TEAM>(a, s, w, o, e0, e1, scores);
     if (TEAM != 32 && size == 1 && t == 0) begin_row<T>(a.x, a.N, row + a.under_way, TEAM * kUnroll);
     Tm::sync();
     distill_list_grad<T, TEAM>(a, s, w, o, e0, e1, list, twice);

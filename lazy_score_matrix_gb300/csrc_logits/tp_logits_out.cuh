@@ -51,8 +51,9 @@ __device__ __forceinline__ Source<T> from_row(const T* p, int M, const T* o) {
     return s;
 }
 
-// The whole vectors of a range of the gradient row o, and the first chunk of their scores, under way.
-template <class T, int TEAM, bool STREAM>
+// The whole vectors of a range of the gradient row o, and the first chunk of their scores, under way. AHEAD: the chunks
+// after it are brought into the L2 cache in bulk (RowVecs::ahead); not for scores that lie there already.
+template <class T, int TEAM, bool STREAM, bool AHEAD = false>
 struct Fetch {
     static constexpr int V = Elem<T>::kVec;
     const Source<T>& from;
@@ -60,7 +61,15 @@ struct Fetch {
     uint4 next[kUnroll];
     __device__ __forceinline__ Fetch(const T* o, int e0, int e1, const Source<T>& from_) : from(from_), off(off_of(o)) {
         ja = max((e0 + off + V - 1) / V, from.lo), jb = max(ja, min((e1 + off) / V, from.hi));
-        if (STREAM) load(ja + Team<TEAM>::tid());  // shared memory needs no head start
+        load(ja + Team<TEAM>::tid());
+        ahead(ja, ja + TEAM * kUnroll);
+    }
+    // vectors j - TEAM kUnroll + kAhead chunks on, or those from `from_j` to there
+    __device__ __forceinline__ void ahead(int j, int from_j) const {
+        if (!AHEAD || TEAM == 32 || threadIdx.x != 0) return;
+        const int j1 = min(j + (1 + kAhead) * TEAM * kUnroll, jb);
+        if (from_j < j1)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from.q + from_j), "r"((j1 - from_j) * 16) : "memory");
     }
     __device__ __forceinline__ void load(int j) {
         if (j + (kUnroll - 1) * TEAM < jb) {
@@ -76,18 +85,18 @@ struct Fetch {
 
 // o[e] = f(score e) for e0 <= e < e1. f(float[V], e) turns the scores of e .. e + V - 1 into gradients. Whole
 // vectors are written as such; what e0, e1 or the source's ends cut is done element by element.
-template <class T, int TEAM, bool STREAM, class F>
-__device__ __forceinline__ void map_range(T* o, int e0, int e1, Fetch<T, TEAM, STREAM>& x, F f) {
+template <class T, int TEAM, bool STREAM, bool AHEAD, class F>
+__device__ __forceinline__ void map_range(T* o, int e0, int e1, Fetch<T, TEAM, STREAM, AHEAD>& x, F f) {
     constexpr int V = Elem<T>::kVec;
     const int off = x.off, t = Team<TEAM>::tid(), ja = x.ja, jb = x.jb;
     const Source<T>& from = x.from;
     uint4* out = reinterpret_cast<uint4*>(o - off);
     for (int j = ja + t; j < jb; j += TEAM * kUnroll) {
         uint4 r[kUnroll];
-        if (!STREAM) x.load(j);
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) r[u] = x.next[u];
-        if (STREAM) x.load(j + TEAM * kUnroll);
+        x.load(j + TEAM * kUnroll);
+        x.ahead(j + TEAM * kUnroll, j + (1 + kAhead) * TEAM * kUnroll);
         const bool all = j + (kUnroll - 1) * TEAM < jb;
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
@@ -156,11 +165,11 @@ __device__ __forceinline__ void shares(const DistillArgs& a, ListBuf& l) {
 }
 
 // Gradient of the columns from e0 to e1 as if none were listed; w: the row's weight over T.
-template <class T, int TEAM, bool STREAM>
+template <class T, int TEAM, bool STREAM, bool AHEAD>
 __device__ __forceinline__ void distill_row_grad(const DistillArgs& a, const RowStats& s, float w, T* o, int e0, int e1,
-                                                 Fetch<T, TEAM, STREAM>& x) {
+                                                 Fetch<T, TEAM, STREAM, AHEAD>& x) {
     const float coef = s.coef * w, gm = s.gm, gls2 = s.gls * kLog2e, c = a.sc.c;
-    map_range<T, TEAM, STREAM>(o, e0, e1, x, [&](float* f, int) {
+    map_range<T, TEAM>(o, e0, e1, x, [&](float* f, int) {
 #pragma unroll
         for (int i = 0; i < Elem<T>::kVec; ++i) f[i] = coef * ex2(fmaf(f[i] - gm, c, -gls2));
     });
