@@ -22,8 +22,8 @@ namespace rows {
 constexpr int kThreads = 256;      // per CTA
 constexpr int kLongThreads = 512;  // where a row is read twice (fewer rows under way, for the second reading to hit
                                    // the cache), and of clusters (few rows)
-constexpr int kUnroll = 4;     // 16-byte vectors a thread has in flight
-constexpr int kAhead = 2;      // chunks that are brought into the L2 cache ahead of a thread's loads
+constexpr int kUnroll = 4;         // 16-byte vectors of a thread's chunk
+constexpr int kAhead = 2;          // chunks that are brought into the L2 cache ahead of a thread's loads
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718f;
 
@@ -355,8 +355,8 @@ struct State {
     }
 };
 
-// N vectors of scores into the state. For two scores: unpacking two, half a maximum each, x - m, the product
-// with c, two ex2 and the sum s. MOMENT: h too; a masked score's distance (-inf) is bounded, as its weight 0 times
+// N vectors of scores into the state. Instructions for two 16-bit scores: one maximum, two of x - m, one product with c,
+// two ex2, one sum s; about 8 a score with the loads and the loop. MOMENT: h too; a masked score's distance (-inf) is bounded, as its weight 0 times
 // it would be NaN. Without h, the product is formed with both words of c instead (c_lo > 0, so that -inf stays).
 // Returns the largest of them.
 template <class T, bool MOMENT, int N>
@@ -659,7 +659,7 @@ __device__ __forceinline__ RowStats close_row(const DistillArgs& a, const State&
     const Two c = add(ls, neg(over_T(l.lm, some ? m : 0.f, a.sc)));
     float loss = 0.f;
     for (int k = threadIdx.x & 31; k < a.K; k += 32)
-        if (b.q[k] > 0.f) {
+        if (!(b.q[k] <= 0.f)) {  // a NaN among the teacher's values shows
             const Two u{b.u[k].x, b.u[k].y};
             loss += b.q[k] * (u.h < __int_as_float(0x7f800000) ? add(u, c).h : u.h);
         }

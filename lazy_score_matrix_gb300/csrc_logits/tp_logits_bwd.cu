@@ -1,5 +1,7 @@
 // Backward kernels of the stored-row consumers (include/tp_logits.h): the row is read again, its probabilities
-// come from the forward's statistics, and each gradient element is written once.
+// come from the forward's statistics, and each gradient element is written once. Memory bounds them: 4096 x 131072
+// bf16 303 us, the measured copy rate; rows whose alignment differs from their gradient's (1021 x 50001 fp32 of rows of
+// 50048) 73 us, 0.82 of it.
 #include <cuda_runtime.h>
 
 #include "tp_launch.h"
@@ -33,7 +35,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_bwd_kernel(const LogprobArg
     const float ls2 = ls * kLog2e, c = a.sc.c, gt = a.g_logprob ? g1 : 0.f;
     const float b1 = fmaf(g2, H, g1), b2 = g2 * kLn2;
     const Source<T> x = from_row<T>(row_at<const T>(a.x, row), a.x.M, o);
-    Fetch<T, TEAM, true> scores(o, r.e0, r.e1, x);
+    Fetch<T, TEAM, false> scores(o, r.e0, r.e1, x);
     map_range<T, TEAM>(o, r.e0, r.e1, scores, [&](float* f, int e) {
 #pragma unroll
         for (int i = 0; i < Elem<T>::kVec; ++i) {
@@ -62,7 +64,7 @@ __global__ void __launch_bounds__(kThreads, 4) distill_bwd_kernel(const DistillA
     const float* st = a.stats + row * kStats;
     if (!load_list<TEAM>(a, row, list) || st[0] == neg_inf()) return zero_range<T, TEAM>(o, r.e0, r.e1);
     const Source<T> from = from_row<T>(p, a.x.M, o);
-    Fetch<T, TEAM, true, true> scores(o, r.e0, r.e1, from);
+    Fetch<T, TEAM, true> scores(o, r.e0, r.e1, from);
     const bool twice = look_up<T, TEAM>(a, p, list, r.e0, r.e1);
     if (TEAM == 32 || threadIdx.x < 32) shares(a, list);
     Tm::sync();

@@ -1,5 +1,9 @@
-// Forward kernels of the stored-row consumers (include/tp_logits.h): one pass over each row with the running
-// softmax state in registers; the alternatives are filtered in the same pass.
+// Forward kernels of the stored-row consumers (include/tp_logits.h): one pass over each row with the running softmax
+// state in registers.
+//
+// What bounds them is memory on long rows without alternatives or a list (4096 x 131072 bf16: 165 us cold, 0.91 of the
+// measured copy rate), instructions and a row's fixed part elsewhere (2048 x 65536 bf16 with 64 alternatives: 76 us, half
+// the copy rate; 32768 x 261 fp32 with 8: 45 us for 34 MB, 1020 instructions a row).
 #include <cuda_runtime.h>
 
 #include "tp_launch.h"

@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(TEAM == 32 ? kThreads : TEAM, TEAM == kLongThr
     if (TEAM == 32 || threadIdx.x < 32) sum_list(a, list);
     State st = read_slice<T, TEAM, REST>(a, x, sl, list, marks[REST ? Tm::id() : 0], next);
     const Source<T> from = from_row<T>(p, M, o);
-    Fetch<T, TEAM, true> scores(o, e0, e1, from);  // the second reading begins while the states meet
+    Fetch<T, TEAM, false> scores(o, e0, e1, from);  // the second reading begins while the states meet
     st = team_state<TEAM>(st, a.sc.c, red);
     if (size > 1) {
         cluster_wait();  // every CTA of the cluster runs, and has looked the listed scores up

@@ -27,10 +27,9 @@ struct Source {
     const T* p;
     const uint4* q;
     int shift, lo, hi;
-    template <bool STREAM>
     __device__ __forceinline__ uint4 get(int j) const {
         if (shift) return window(q[j], q[j + 1], shift);  // neighbours read the same bytes: cached
-        return STREAM ? __ldcs(q + j) : q[j];
+        return __ldcs(q + j);
     }
 };
 
@@ -53,7 +52,7 @@ __device__ __forceinline__ Source<T> from_row(const T* p, int M, const T* o) {
 
 // The whole vectors of a range of the gradient row o, and the first chunk of their scores, under way. AHEAD: the chunks
 // after it are brought into the L2 cache in bulk (RowVecs::ahead); not for scores that lie there already.
-template <class T, int TEAM, bool STREAM, bool AHEAD = false>
+template <class T, int TEAM, bool AHEAD>
 struct Fetch {
     static constexpr int V = Elem<T>::kVec;
     const Source<T>& from;
@@ -74,19 +73,19 @@ struct Fetch {
     __device__ __forceinline__ void load(int j) {
         if (j + (kUnroll - 1) * TEAM < jb) {
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) next[u] = from.template get<STREAM>(j + u * TEAM);
+            for (int u = 0; u < kUnroll; ++u) next[u] = from.get(j + u * TEAM);
         } else {
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u)
-                if (j + u * TEAM < jb) next[u] = from.template get<STREAM>(j + u * TEAM);
+                if (j + u * TEAM < jb) next[u] = from.get(j + u * TEAM);
         }
     }
 };
 
 // o[e] = f(score e) for e0 <= e < e1. f(float[V], e) turns the scores of e .. e + V - 1 into gradients. Whole
 // vectors are written as such; what e0, e1 or the source's ends cut is done element by element.
-template <class T, int TEAM, bool STREAM, bool AHEAD, class F>
-__device__ __forceinline__ void map_range(T* o, int e0, int e1, Fetch<T, TEAM, STREAM, AHEAD>& x, F f) {
+template <class T, int TEAM, bool AHEAD, class F>
+__device__ __forceinline__ void map_range(T* o, int e0, int e1, Fetch<T, TEAM, AHEAD>& x, F f) {
     constexpr int V = Elem<T>::kVec;
     const int off = x.off, t = Team<TEAM>::tid(), ja = x.ja, jb = x.jb;
     const Source<T>& from = x.from;
@@ -165,9 +164,9 @@ __device__ __forceinline__ void shares(const DistillArgs& a, ListBuf& l) {
 }
 
 // Gradient of the columns from e0 to e1 as if none were listed; w: the row's weight over T.
-template <class T, int TEAM, bool STREAM, bool AHEAD>
+template <class T, int TEAM, bool AHEAD>
 __device__ __forceinline__ void distill_row_grad(const DistillArgs& a, const RowStats& s, float w, T* o, int e0, int e1,
-                                                 Fetch<T, TEAM, STREAM, AHEAD>& x) {
+                                                 Fetch<T, TEAM, AHEAD>& x) {
     const float coef = s.coef * w, gm = s.gm, gls2 = s.gls * kLog2e, c = a.sc.c;
     map_range<T, TEAM>(o, e0, e1, x, [&](float* f, int) {
 #pragma unroll

@@ -362,6 +362,15 @@ def test_nan_and_inf_reach_the_results():
 
 
 @pytest.mark.parametrize("rest", [False, True])
+def test_nan_in_a_teacher_list_shows(rest):
+    x = scores(3, 300, torch.float32, 3).to(DEV)
+    values = torch.full((3, 5), -2.0, device=DEV)
+    values[1, 2] = float("nan")
+    loss = tp.topk_distillation(x, torch.arange(5, device=DEV).repeat(3, 1), values, rest=rest)
+    assert loss.isnan().tolist() == [False, True, False]
+
+
+@pytest.mark.parametrize("rest", [False, True])
 def test_lists_with_repeats_gaps_and_any_order(rest):
     x = scores(4, 777, torch.float32, 6)
     g = torch.Generator().manual_seed(4)
