@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const DistillArgs 
     x.load(next, sl.begin + t, TEAM, sl.end);
     if (TEAM != 32 && t == 0) x.ahead(sl.begin + TEAM * kUnroll, TEAM * kUnroll, sl.end, true);
     look_up<T, TEAM>(a, p, list, 0, a.x.M);
-    if (rank == 0 && (TEAM == 32 || threadIdx.x < 32)) sum_list(a, list);
+    if (rank == 0) sum_list<TEAM>(a, list);
     State st = read_slice<T, TEAM, REST>(a, x, sl, list, marks[REST ? Tm::id() : 0], next);
     st = team_state<TEAM>(st, a.sc.c, red);
     if (size > 1) {

@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(TEAM == 32 ? kThreads : TEAM, TEAM == kLongThr
     x.load(next, sl.begin + t, TEAM, sl.end);
     if (TEAM != 32 && t == 0) x.ahead(sl.begin + TEAM * kUnroll, TEAM * kUnroll, sl.end, true);
     const bool twice = look_up<T, TEAM>(a, p, list, 0, M);
-    if (TEAM == 32 || threadIdx.x < 32) sum_list(a, list);
+    sum_list<TEAM>(a, list);
     State st = read_slice<T, TEAM, REST>(a, x, sl, list, marks[REST ? Tm::id() : 0], next);
     const Source<T> from = from_row<T>(p, M, o);
     Fetch<T, TEAM, false> scores(o, e0, e1, from);  // the second reading begins while the states meet

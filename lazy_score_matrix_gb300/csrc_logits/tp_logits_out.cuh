@@ -140,7 +140,7 @@ __device__ __forceinline__ Range range_of(const T* o, int M, int rank, int parts
     return Range{max(first_of(o, s.begin), 0), min(first_of(o, s.end), M)};
 }
 
-// The teacher's shares into l.q, by one warp (what distill_row leaves there, in fp32).
+// The teacher's shares into l.q and their scale, by one warp (what sum_list leaves there, in fp32).
 __device__ __forceinline__ void shares(const DistillArgs& a, ListBuf& l) {
     const int lane = threadIdx.x & 31;
     float y[4], top = a.rest ? 0.f : neg_inf(), sum = 0.f;
@@ -160,7 +160,8 @@ __device__ __forceinline__ void shares(const DistillArgs& a, ListBuf& l) {
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        if (lane + 32 * j < a.K) l.q[lane + 32 * j] = a.rest ? y[j] : y[j] / sum;
+        if (lane + 32 * j < a.K) l.q[lane + 32 * j] = y[j];
+    if (lane == 0) l.sums.scale = a.rest ? 1.f : 1.f / sum;
 }
 
 // Gradient of the columns from e0 to e1 as if none were listed; w: the row's weight over T.
@@ -183,6 +184,7 @@ __device__ __forceinline__ void distill_list_grad(const DistillArgs& a, const Ro
         if (twice)
             for (int j = k + 1; j < a.K; ++j)
                 if (l.id[j] == l.id[k]) q += l.q[j];
+        q *= l.sums.scale;
         o[l.id[k]] = Elem<T>::put(w * (s.Z * expf((l.x[k] - s.m) * a.sc.inv - s.ls) - q));
     }
 }
