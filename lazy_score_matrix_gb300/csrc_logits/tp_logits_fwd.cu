@@ -25,7 +25,7 @@ struct TopBuf {
     static constexpr int kKeep = TEAM == 32 ? 96 : kMaxList + 32;       // keys after a cut, at most
     static constexpr int kCap = TEAM == 32 ? 256 : kMaxCluster * kKeep;  // room for what a cluster's CTAs keep
     static constexpr int kSlots = TEAM == kLongThreads ? 8 : 16, kWork = TEAM == 32 ? 128 : 1024;
-    unsigned long long key[kCap];
+    alignas(16) unsigned long long key[kCap];
     unsigned long long thr;  // keys at or below it cannot be among the best
     float chunk[kSlots][TEAM];      // largest score of the thread's chunks, `each` of them to a slot
     unsigned short work[kWork];     // slots to look at again: slot * TEAM + thread
@@ -122,9 +122,9 @@ struct Tops {
     // The columns that reach the bar, to the buffer, by way of the chunks that do. false: there was not room for all.
     // Slots hold `each` chunks; the slice begins at vector `begin`.
     template <class T>
-    __device__ __forceinline__ bool collect(const RowVecs<T>& x, int begin, int end, int each, float bar) {
+    __device__ __forceinline__ bool collect(const RowVecs<T>& x, int begin, int end, int slots, int each, float bar) {
         constexpr int V = Elem<T>::kVec;
-        const int t = Team<TEAM>::tid(), chunk = TEAM * kUnroll, slots = (end - begin + each * chunk - 1) / (each * chunk);
+        const int t = Team<TEAM>::tid(), chunk = TEAM * kUnroll;
         for (int i = 0; i < slots; ++i)
             if (b.chunk[i][t] >= bar) {
                 const int at = atomicAdd(&b.todo, 1);
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(TEAM == 32 ? kThreads : TEAM, TEAM == kLongThr
             for (int r = 0; r < size; ++r) bound = max(bound, bounds[r]);  // each holds for the whole row
     }
     if (TOP) {
-        if (!best.template collect<T>(x, sl.begin, sl.end, each, bound ? of_ord(bound) : lowest())) {
+        if (!best.template collect<T>(x, sl.begin, sl.end, slot, each, bound ? of_ord(bound) : lowest())) {
             Tm::sync();
             if (t == 0) best.b.cnt = 0, best.b.thr = bound ? ((unsigned long long)bound << 32) - 1 : 0;
             Tm::sync();
@@ -311,8 +311,13 @@ __global__ void __launch_bounds__(TEAM == 32 ? kThreads : TEAM, TEAM == kLongThr
         const int n = best.b.cnt;
         for (int i = t; i < n; i += TEAM) {  // the keys differ: a key's place is the number of larger ones
             const unsigned long long k = best.b.key[i];
-            int place = 0;
-            for (int j = 0; j < n; ++j) place += best.b.key[j] > k;
+            int place = n & 1 ? best.b.key[n - 1] > k : 0;
+            const ulonglong2* pair = reinterpret_cast<const ulonglong2*>(best.b.key);
+#pragma unroll 4
+            for (int j = 0; j < n / 2; ++j) {
+                const ulonglong2 p = pair[j];
+                place += (p.x > k) + (p.y > k);
+            }
             if (place < a.top) {
                 a.top_logprobs[row * a.top + place] = (of_ord((uint32_t)(k >> 32)) - st.m) * a.sc.inv - ls;
                 a.top_ids[row * a.top + place] = (int64_t)(~(uint32_t)k);

@@ -4,7 +4,7 @@
 //
 // What bounds it is memory, as long as the rows under way on the whole card fit the cache (kCacheBytes) and are
 // enough to cover the time between a row's last load and its first store. Measured on 8192 x 131072 bf16 (floor
-// 618 us at the measured copy rate): two CTAs of 512 an SM 701 us; one of 1024 957 us (nothing covers the
+// 618 us at the measured copy rate): two CTAs of 512 an SM 715 us; one of 1024 957 us (nothing covers the
 // reduction); four CTAs an SM with the row's slices in the shared memory of a cluster of four 1100 us (the
 // start of a cluster waits for four free places at once), and with slices half as long 2218 us.
 #include <cuda_runtime.h>

@@ -689,6 +689,26 @@ def test_outputs_stay_inside_their_buffers():
         assert not (inner == -77).any(), name
 
 
+@pytest.mark.parametrize("entry", ["token_logprobs", "token_logprobs_backward", "topk_distillation", "topk_distillation_backward",
+                                   "topk_distillation_grad"])
+def test_a_failed_call_raises_and_leaves_the_process_usable(entry, monkeypatch):
+    x = scores(4, 300, torch.float32, 3).to(DEV)
+    ids, values = (t.to(DEV) for t in teacher_list(x.cpu(), 4, 1.0, False, 3))
+
+    def step():
+        leaf = x.detach().requires_grad_(True)
+        (tp.token_logprobs(leaf, ids[:, 0]).logprobs.sum() + tp.topk_distillation(leaf, ids, values).sum()).backward()
+        return leaf.grad, tp.topk_distillation_grad(x, ids, values)[1]
+
+    want = step()
+    monkeypatch.setenv("TP_FAULT_INJECT", entry)
+    with pytest.raises(_lib.TPError) as e:
+        step()
+    assert e.value.status == _lib.TP_ERR_CUDA and entry in str(e.value)
+    monkeypatch.delenv("TP_FAULT_INJECT")
+    assert all(torch.equal(a, b) for a, b in zip(step(), want))
+
+
 def test_refusals():
     x = torch.zeros(4, 50, device=DEV)
     tok, ids, val = torch.zeros(4, dtype=torch.int64, device=DEV), torch.zeros(4, 3, dtype=torch.int64, device=DEV), torch.zeros(4, 3, device=DEV)
