@@ -2,7 +2,7 @@
 // autograd functions and the libtp call. Nothing here computes on the data.
 //
 // In C++, unlike the ctypes binding of tp.h: these calls sit in decoding loops and training steps where a kernel
-// takes 10 us. A call through ctypes and torch's Python API cost 20 us of the caller's time on the GPU machine's cores and
+// takes 10 us. A call through ctypes and torch's Python API cost 20 us of the caller's time on a Grace core and
 // a Python autograd function 110 us more than a native one, most of it for moving the interpreter's data to autograd's
 // thread and back.
 #include <c10/cuda/CUDAGuard.h>
