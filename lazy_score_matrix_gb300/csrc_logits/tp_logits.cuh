@@ -393,9 +393,9 @@ __device__ __forceinline__ float add_scores(State& st, const uint4 (&r)[N], cons
 }
 
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v = max_nan(v, __shfl_xor_sync(~0u, v, o));
-    return v;
+    float r;
+    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 // sum of the (already aligned) states of a warp, in every lane
 __device__ __forceinline__ void warp_sum(State& st) {
