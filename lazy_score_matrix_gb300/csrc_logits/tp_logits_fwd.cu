@@ -3,7 +3,7 @@
 //
 // What bounds them is memory on long rows without alternatives or a list (4096 x 131072 bf16: 165 us cold, 0.91 of the
 // measured copy rate), instructions and a row's fixed part elsewhere (2048 x 65536 bf16 with 64 alternatives: 76 us, half
-// the copy rate; 32768 x 261 fp32 with 8: 45 us for 34 MB, 1020 instructions a row).
+// the copy rate; 32768 x 261 fp32 with 8: 31 us for 34 MB).
 #include <cuda_runtime.h>
 
 #include "tp_launch.h"
@@ -192,6 +192,48 @@ __device__ __forceinline__ void leave_out(const LogprobArgs& a, int64_t row, int
     for (int i = t; i < a.top; i += team) a.top_logprobs[row * a.top + i] = neg_inf(), a.top_ids[row * a.top + i] = -1;
 }
 
+// The row's results from its state, the token's score xt (thread 0) and the keys of its best columns; `shared`: a word
+// for the CTA.
+template <int TEAM, bool TOP>
+__device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, const State& st, float xt, Tops<TEAM>& best, float* shared) {
+    const int t = Team<TEAM>::tid();
+    const bool some = st.m != neg_inf();
+    const float z = st.s + (st.lo + a.sc.delta * st.h);
+    float ls = some ? logf(z) : 0.f;
+    if (t == 0) {
+        if (TOP && TEAM != 32) *shared = ls;  // to the other warps
+        const float H = some ? ls - st.h / z * a.sc.inv : 0.f;
+        a.entropy[row] = H;
+        if (a.logprobs) a.logprobs[row] = some ? (xt - st.m) * a.sc.inv - ls : neg_inf();
+        if (a.stats) {
+            float* o = a.stats + row * kStats;
+            o[0] = st.m, o[1] = ls, o[2] = H;
+            for (int i = 3; i < kStats; ++i) o[i] = 0.f;
+        }
+    }
+    if (TOP) {
+        Team<TEAM>::sync();
+        if (best.b.cnt > TopBuf<TEAM>::kKeep) best.cut();
+        if (TEAM != 32) ls = *shared;
+        const int n = best.b.cnt;
+        for (int i = t; i < n; i += TEAM) {  // the keys differ: a key's place is the number of larger ones
+            const unsigned long long k = best.b.key[i];
+            int place = n & 1 ? best.b.key[n - 1] > k : 0;
+            const ulonglong2* pair = reinterpret_cast<const ulonglong2*>(best.b.key);
+#pragma unroll 4
+            for (int j = 0; j < n / 2; ++j) {
+                const ulonglong2 p = pair[j];
+                place += (p.x > k) + (p.y > k);
+            }
+            if (place < a.top) {
+                a.top_logprobs[row * a.top + place] = (of_ord((uint32_t)(k >> 32)) - st.m) * a.sc.inv - ls;
+                a.top_ids[row * a.top + place] = (int64_t)(~(uint32_t)k);
+            }
+        }
+        for (int i = n + t; i < a.top; i += TEAM) a.top_logprobs[row * a.top + i] = neg_inf(), a.top_ids[row * a.top + i] = -1;
+    }
+}
+
 struct Gather {  // the candidates of a cluster's CTAs, in the first of them
     static constexpr int kMost = TopBuf<kLongThreads>::kKeep;
     unsigned long long key[kMaxCluster][kMost];
@@ -291,40 +333,76 @@ __global__ void __launch_bounds__(TEAM == 32 ? kThreads : TEAM, TEAM == kLongThr
             if (t == 0) best.b.cnt = at, best.b.thr = 0;
         }
     }
-    const bool some = st.m != neg_inf();
-    const float z = st.s + (st.lo + a.sc.delta * st.h);
-    float ls = some ? logf(z) : 0.f;
-    if (t == 0) {
-        if (TOP) red.s[0] = ls;  // to the other warps
-        const float H = some ? ls - st.h / z * a.sc.inv : 0.f;
-        a.entropy[row] = H;
-        if (a.logprobs) a.logprobs[row] = some ? (Elem<T>::get(x.p[tok]) - st.m) * a.sc.inv - ls : neg_inf();
-        if (a.stats) {
-            float* o = a.stats + row * kStats;
-            o[0] = st.m, o[1] = ls, o[2] = H;
-            for (int i = 3; i < kStats; ++i) o[i] = 0.f;
-        }
-    }
+    write_row<TEAM, TOP>(a, row, st, t == 0 ? Elem<T>::get(x.p[tok]) : 0.f, best, red.s);
+}
+
+// Short rows, a warp each, one score a register: no vectors, so no edges of any, and the maximum before the first
+// exponential. 32768 x 261 fp32 with 8 alternatives: 31 us, 42 by logprobs_kernel; without any 17 and 24. At 500 columns
+// 36 and 43 us, bf16 41 and 48; with PER = 16 for all lengths 100 columns took 33 us instead of 25. Fewer registers for
+// more rows under way: 39 us with five CTAs an SM, 44 with six, 50 with eight.
+constexpr int kShort = 512;
+template <class T, bool TOP, int PER>
+__global__ void __launch_bounds__(kThreads, 4) logprobs_short_kernel(const LogprobArgs a) {
+    using Tm = Team<32>;
+    __shared__ TopBuf<32> tops[TOP ? Tm::kPerCta : 1];
+    const int64_t row = (int64_t)blockIdx.x * Tm::kPerCta + Tm::id();
+    if (row >= a.N) return;
+    const int t = Tm::tid(), M = a.x.M;
+    const int64_t tok = a.tokens ? a.tokens[row] : 0;
+    if (tok < 0 || tok >= M) return leave_out(a, row, t, 32);
+    const T* p = row_at<const T>(a.x, row);
+    float f[PER], own = neg_inf();
+#pragma unroll
+    for (int i = 0; i < PER; ++i) f[i] = t + 32 * i < M ? Elem<T>::get(__ldcg(p + t + 32 * i)) : neg_inf();
+    const float xt = t == 0 ? Elem<T>::get(p[tok]) : 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) own = max_nan(own, f[i]);
+    State st;
+    st.m = warp_max(own);
+    Tops<32> best(tops[TOP ? Tm::id() : 0], a.top);
     if (TOP) {
-        best.cut();
-        if (TEAM != 32) ls = red.s[0];
-        const int n = best.b.cnt;
-        for (int i = t; i < n; i += TEAM) {  // the keys differ: a key's place is the number of larger ones
-            const unsigned long long k = best.b.key[i];
-            int place = n & 1 ? best.b.key[n - 1] > k : 0;
-            const ulonglong2* pair = reinterpret_cast<const ulonglong2*>(best.b.key);
-#pragma unroll 4
-            for (int j = 0; j < n / 2; ++j) {
-                const ulonglong2 p = pair[j];
-                place += (p.x > k) + (p.y > k);
+        best.clear();
+        const uint32_t bound = best.bound(own, sizeof(T) == 2 ? 1u << 12 : 1u);
+        const float bar = bound ? of_ord(bound) : lowest();
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const bool in = f[i] >= bar;
+            const uint32_t who = __ballot_sync(~0u, in);
+            if (who == 0) continue;
+            if (32 * i >= TopBuf<32>::kCap && n + __popc(who) > TopBuf<32>::kCap) {
+                if (t == 0) best.b.cnt = n;
+                best.cut();
+                n = best.b.cnt;
+                __syncwarp();  // all have read it
             }
-            if (place < a.top) {
-                a.top_logprobs[row * a.top + place] = (of_ord((uint32_t)(k >> 32)) - st.m) * a.sc.inv - ls;
-                a.top_ids[row * a.top + place] = (int64_t)(~(uint32_t)k);
-            }
+            if (in) best.b.key[n + __popc(who & ((1u << t) - 1))] = key_of(f[i], t + 32 * i);
+            n += __popc(who);
         }
-        for (int i = n + t; i < a.top; i += TEAM) a.top_logprobs[row * a.top + i] = neg_inf(), a.top_ids[row * a.top + i] = -1;
+        if (t == 0) best.b.cnt = n;  // read after a barrier, in write_row
     }
+    if (st.m != neg_inf()) {
+        float2 s = make_float2(0.f, 0.f), h = s;
+#pragma unroll
+        for (int i = 0; i < PER; i += 2) {
+            if (32 * i >= M) break;
+            float2 d = sub2(make_float2(f[i], f[i + 1]), st.m);
+            d = make_float2(max_nan(d.x, -1e30f), max_nan(d.y, -1e30f));
+            const float2 x = mul2(d, a.sc.c), e = make_float2(ex2(x.x), ex2(x.y));
+            s = add2(s, e), h = fma2(e, d, h);
+        }
+        st.s = s.x + s.y, st.h = h.x + h.y;
+        warp_sum(st);
+    }
+    write_row<32, TOP>(a, row, st, xt, best, nullptr);
+}
+
+template <class T, bool TOP>
+void run_short(const LogprobArgs& a, const Shape& sh, cudaStream_t s) {
+    if (a.x.M <= 128) launch(logprobs_short_kernel<T, TOP, 4>, sh, s, a);
+    else if (a.x.M <= 256) launch(logprobs_short_kernel<T, TOP, 8>, sh, s, a);
+    else if (a.x.M <= 384) launch(logprobs_short_kernel<T, TOP, 12>, sh, s, a);
+    else launch(logprobs_short_kernel<T, TOP, 16>, sh, s, a);
 }
 
 template <class T, int TEAM, bool REST>
@@ -386,7 +464,10 @@ void run_logprobs(LogprobArgs a, cudaStream_t s) {
     const bool large = a.top && a.N < kResident;  // few rows with alternatives: CTAs of kLongThreads
     Shape sh = shape_of(a.N, row, a.top <= 32 ? kWarpBytes : 0, large ? kResidentLong : kResident);
     a.under_way = kResident;
-    if (sh.warp) {
+    if (sh.warp && a.x.M <= kShort) {
+        if (a.top) run_short<T, true>(a, sh, s);
+        else run_short<T, false>(a, sh, s);
+    } else if (sh.warp) {
         if (a.top) launch(logprobs_kernel<T, 32, true>, sh, s, a);
         else launch(logprobs_kernel<T, 32, false>, sh, s, a);
     } else if (!a.top) {

@@ -213,6 +213,40 @@ def test_logprobs_shapes(n, m, dtype):
         del x64, d, p, logp, order
 
 
+# Many rows of few columns: one score a register of a warp, at every count of registers and about its ends; ties that let
+# every column through, masked columns, rows left out, rows at odd addresses.
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("m", [1, 2, 31, 32, 33, 127, 128, 129, 255, 256, 257, 289, 384, 385, 511, 512, 513])
+def test_many_short_rows(m, dtype):
+    n, top = 1217, min(m, 32)
+    i = torch.arange(n)
+    x = scores(n, m, dtype, m)
+    x[0::5] = 2.0  # all equal
+    x[1::5] = (torch.arange(m) % 3 * 0.5).to(dtype)
+    x[2::5, ::3] = NEG
+    x[7::50] = NEG
+    x[12::50, 1:] = NEG
+    tok = i * 7 % m
+    tok[4::13] = -100
+    buf = torch.full((n, m + 3), float("nan"), dtype=dtype, device=DEV)
+    buf[:, 1:1 + m] = x.to(DEV)
+    leaf = buf[:, 1:1 + m].detach().requires_grad_(True)
+    r = tp.token_logprobs(leaf, tok.to(DEV), temperature=0.8, top=top)
+    none = tp.token_logprobs(buf[:, 1:1 + m], tok.to(DEV), temperature=0.8)
+    assert torch.equal(none.logprobs, r.logprobs) and torch.equal(none.entropy, r.entropy)
+    order = torch.sort(x.float(), dim=1, descending=True, stable=True).indices[:, :top]
+    order = torch.where((x.float().gather(1, order) > NEG) & (tok >= 0)[:, None], order, -1)
+    assert torch.equal(r.top_ids.cpu(), order)
+    g1, g2 = torch.linspace(-1, 1, n), torch.linspace(0.2, -0.3, n)
+    grad, = torch.autograd.grad((r.logprobs, r.entropy), leaf, (g1.to(DEV), g2.to(DEV)))
+    for k in list(range(26)) + list(range(26, n, 83)) + [n - 1]:
+        w = ref.logprobs(x[k].double(), int(tok[k]), 0.8, top, float(g1[k]), float(g2[k]))
+        ref.close(r.logprobs[k].detach(), w["lp"], w["lp_tol"], what=f"logprob of row {k}")
+        ref.close(r.entropy[k].detach(), w["h"], w["h_tol"], what=f"entropy of row {k}")
+        ref.close(r.top_logprobs[k], w["top_lp"], w["top_tol"], what=f"alternatives of row {k}")
+        ref.close(grad[k], w["grad"], w["grad_tol"], dtype, what=f"gradient of row {k}")
+
+
 @pytest.mark.parametrize("n,m,dtype", SHAPES)
 @pytest.mark.parametrize("rest", [False, True])
 def test_distill_shapes(n, m, dtype, rest):
