@@ -339,7 +339,9 @@ __global__ void __launch_bounds__(TEAM == 32 ? kThreads : TEAM, TEAM == kLongThr
 // Short rows, a warp each, one score a register: no vectors, so no edges of any, and the maximum before the first
 // exponential. 32768 x 261 fp32 with 8 alternatives: 31 us, 42 by logprobs_kernel; without any 17 and 24. At 500 columns
 // 36 and 43 us, bf16 41 and 48; with PER = 16 for all lengths 100 columns took 33 us instead of 25. Fewer registers for
-// more rows under way: 39 us with five CTAs an SM, 44 with six, 50 with eight.
+// more rows under way: 39 us with five CTAs an SM, 44 with six, 50 with eight. Few rows too: 600 x 261 bf16 with 8 alternatives
+// 9 us, 19 with a CTA a row; one row of 32 columns 6 and 10; but 64 x 500 with 32 alternatives 13 and 11. More than 32
+// take more threads than a warp's.
 constexpr int kShort = 512;
 template <class T, bool TOP, int PER>
 __global__ void __launch_bounds__(kThreads, 4) logprobs_short_kernel(const LogprobArgs a) {
@@ -464,7 +466,8 @@ void run_logprobs(LogprobArgs a, cudaStream_t s) {
     const bool large = a.top && a.N < kResident;  // few rows with alternatives: CTAs of kLongThreads
     Shape sh = shape_of(a.N, row, a.top <= 32 ? kWarpBytes : 0, large ? kResidentLong : kResident);
     a.under_way = kResident;
-    if (sh.warp && a.x.M <= kShort) {
+    if (a.x.M <= kShort && a.top <= 32) {
+        sh.cluster = 1, sh.grid = (unsigned)((a.N + 7) / 8);
         if (a.top) run_short<T, true>(a, sh, s);
         else run_short<T, false>(a, sh, s);
     } else if (sh.warp) {
