@@ -16,8 +16,9 @@
  *   - Scores are fp32, fp16 or bf16; probabilities, sums and statistics are fp32 or wider; gradients have
  *     the scores' type (one rounding at the end).
  *   - A score of -inf is a masked column: probability 0, gradient 0, never an alternative. A row of -inf
- *     alone has log probability -inf, entropy 0, no alternatives and gradient 0. NaN or +inf in a row that
- *     is read gives NaN in its results; nothing else is promised for them.
+ *     alone has log probability -inf, entropy 0, no alternatives and gradient 0. The type's lowest value is a
+ *     score like any other, at any temperature: its probability is 0 beside an ordinary one, its distance
+ *     finite. NaN or +inf in a row that is read gives NaN in its results; nothing else is promised for them.
  *   - Rows left out (a token, or a whole list, that does not count) are not read: zeros, (-inf, -1), and a
  *     zero gradient, whatever the row holds.
  *   - Results do not depend on the run: no atomics on floating data, the same call gives the same bits.

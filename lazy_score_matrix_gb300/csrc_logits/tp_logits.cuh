@@ -536,11 +536,21 @@ __device__ __forceinline__ bool look_up(const DistillArgs& a, const T* p, ListBu
     return twice;
 }
 
-// (x - m)/T; one word where it is -inf, or as good as
+// (x - m)/T; one word where it is -inf, or as good as. That word may be -inf for a finite x (the lowest value over T < 1),
+// so what goes on to a sum is asked far_below first.
 __device__ __forceinline__ Two over_T(float x, float m, const Scale& sc) {
     const float d = x - m;
     if (!(d > -1e30f)) return Two{d * sc.inv, 0.f};
     return mul(two_sum(x, -m), Two{sc.inv, sc.inv_lo});
+}
+// Whether x lies so far below a finite maximum m that its distance is all that counts beside logarithms of sums (and
+// its probability is 0); false where either is NaN.
+__device__ __forceinline__ bool far_below(float x, float m) { return x - m <= -1e30f && m < __int_as_float(0x7f800000); }
+// q (m - x)/T 2^-64 for such an x and q > 0: neither the distance nor its quotient needs to be in fp32's range, where the
+// product is. +inf for a masked x.
+__device__ __forceinline__ float far_term(const Two& q, float x, float m, const Scale& sc) {
+    if (x == neg_inf()) return -x;
+    return mul(q, mul(two_sum(m * 0x1p-64f, -x * 0x1p-64f), Two{sc.inv, sc.inv_lo})).h;
 }
 
 // The list's sums into l.sums, and its entries' q and u; by the warps that hold an entry a thread, whose first does the
@@ -659,29 +669,42 @@ __device__ __forceinline__ RowStats close_row(const DistillArgs& a, const State&
     }
     const bool some = m != neg_inf();
     const Two ls = some ? ln_two(z) : Two{0.f, 0.f};
-    // scale sum q (log q - (x - lm)/T + c), c = ln z - (lm - m)/T - ln of the q's sum
+    // scale sum q (log q - (x - lm)/T + c), c = ln z - (lm - m)/T - ln of the q's sum; c is of use unless all of the list
+    // is far below m
     const Two c = add(add(ls, neg(over_T(l.lm, some ? m : 0.f, a.sc))), neg(l.ln));
-    float loss = 0.f;
+    float loss = 0.f, far = 0.f;
     for (int k = threadIdx.x & 31; k < a.K; k += 32)
         if (!(b.q[k] <= 0.f)) {  // a NaN among the teacher's values shows
             const Two u{b.u[k].x, b.u[k].y};
-            loss += b.q[k] * (u.h < __int_as_float(0x7f800000) ? add(u, c).h : u.h);
+            if (far_below(b.x[k], m)) far += far_term(Two{b.q[k], b.q_lo[k]}, b.x[k], m, a.sc);
+            else loss += b.q[k] * (u.h < __int_as_float(0x7f800000) ? add(u, c).h : u.h);
         }
 #pragma unroll
     for (int o = 16; o; o >>= 1) loss += __shfl_xor_sync(~0u, loss, o);
     loss *= l.scale;
+    if (__any_sync(~0u, far != 0.f)) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) far += __shfl_xor_sync(~0u, far, o);
+        loss += far * l.scale * 0x1p64f;
+    }
     RowStats s;
     s.m = s.gm = m, s.ls = s.gls = ls.h, s.coef = l.Z.h, s.Z = l.Z.h;
     if (a.rest) {
         s.coef = 0.f;
         if (st.m != neg_inf()) {
-            const Two lr = ln_two(zs), lp = add(add(over_T(st.m, m, a.sc), lr), neg(ls));  // log p_r
-            if (l.q_r > 0.f) loss += l.q_r * add(l.q_r_ln, neg(lp)).h;
-            const Two Z = add(l.Z, Two{l.q_r, 0.f});
-            s.gm = st.m, s.gls = lr.h, s.Z = Z.h, s.coef = add(mul(Z, exp_two(lp)), Two{-l.q_r, 0.f}).h;
+            const Two lr = ln_two(zs), Z = add(l.Z, Two{l.q_r, 0.f});
+            s.gm = st.m, s.gls = lr.h, s.Z = Z.h;
+            if (far_below(st.m, m)) {  // p_r = 0
+                if (l.q_r > 0.f) loss += far_term(Two{l.q_r, 0.f}, st.m, m, a.sc) * 0x1p64f;
+                s.coef = -l.q_r;
+            } else {
+                const Two lp = add(add(over_T(st.m, m, a.sc), lr), neg(ls));  // log p_r
+                if (l.q_r > 0.f) loss += l.q_r * add(l.q_r_ln, neg(lp)).h;
+                s.coef = add(mul(Z, exp_two(lp)), Two{-l.q_r, 0.f}).h;
+            }
         }
     }
-    if (m != m) loss = m;
+    if (!(m < __int_as_float(0x7f800000))) loss = m - m;  // NaN
     s.loss = loss;
     return s;
 }
