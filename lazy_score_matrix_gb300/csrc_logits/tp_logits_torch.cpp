@@ -1,5 +1,5 @@
 // PyTorch binding of include/tp_logits.h: argument checks, outputs from PyTorch's allocator, the current stream, the
-// autograd functions and the libtp call. Nothing here computes on the data.
+// autograd functions and the libtp call, as operators of PyTorch's dispatcher. Nothing here computes on the data.
 //
 // In C++, unlike the ctypes binding of tp.h: these calls sit in decoding loops and training steps where a kernel
 // takes 10 us. A call through ctypes and torch's Python API cost 20 us of the caller's time on a Grace core and
@@ -9,6 +9,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/extension.h>
+#include <torch/library.h>
 
 #include <array>
 #include <optional>
@@ -56,16 +57,19 @@ struct Rows {
     Tensor t;  // what r points into: a contiguous copy where the strides need one
 };
 
+void check_device(const Tensor& t) { TORCH_CHECK_VALUE(t.is_cuda() || t.is_meta(), "libtp runs on CUDA tensors only (no CPU fallback)"); }
+
+tp_rows_dtype check_rows_type(const Tensor& t, const char* name) {
+    const auto type = t.scalar_type();
+    TORCH_CHECK_TYPE(type == at::kFloat || type == at::kHalf || type == at::kBFloat16, name,
+                     " must be a float32, float16 or bfloat16 tensor, got ", type);
+    TORCH_CHECK_VALUE(t.dim() >= 1 && t.size(-1) >= 1, name, " must have shape [..., M] with M >= 1, got ", t.sizes());
+    return type == at::kFloat ? TP_ROWS_F32 : type == at::kHalf ? TP_ROWS_F16 : TP_ROWS_BF16;
+}
+
 Rows rows_of(const Tensor& t, const char* name, bool copy = true) {
     tp_rows r{};
-    switch (t.scalar_type()) {
-        case at::kFloat: r.dtype = TP_ROWS_F32; break;
-        case at::kHalf: r.dtype = TP_ROWS_F16; break;
-        case at::kBFloat16: r.dtype = TP_ROWS_BF16; break;
-        default: TORCH_CHECK_TYPE(false, name, " must be a float32, float16 or bfloat16 tensor, got ", t.scalar_type());
-    }
-    TORCH_CHECK_VALUE(t.dim() >= 1 && t.size(-1) >= 1, name, " must have shape [..., M] with M >= 1, got ", t.sizes());
-    TORCH_CHECK_VALUE(t.is_cuda(), "libtp runs on CUDA tensors only (no CPU fallback)");
+    r.dtype = check_rows_type(t, name);
     r.M = t.size(-1);
     r.N = t.numel() / r.M;
     Tensor kept = t;
@@ -79,6 +83,9 @@ Rows rows_of(const Tensor& t, const char* name, bool copy = true) {
     r.data = kept.data_ptr();
     return Rows{r, std::move(kept)};
 }
+
+// the logits as a backward keeps them: a copy where rows_of would make one, once for both directions
+Tensor readable(const Tensor& t) { return row_strides(t) ? t : t.contiguous(); }
 
 tp_rows dense(const tp_rows& like, const Tensor& t) {
     tp_rows r = like;
@@ -120,88 +127,169 @@ Tensor once(Tensor g) {
     return (*e)({g.detach().set_requires_grad(true)})[0];
 }
 
-Tensor dense_grad(const Tensor& g) { return g.defined() ? g.contiguous() : g; }
+OptTensor maybe(const Tensor& t) { return t.defined() ? OptTensor(t) : std::nullopt; }
+
+// --- operators ---------------------------------------------------------------------------------------------------
+//
+// Calls go through PyTorch's dispatcher as operators with a schema, so that whatever records calls (jit.trace, make_fx) records
+// them, runs them again on replay and finds their gradients there, and fake tensors get shapes. Outside the dispatcher a
+// trace would hold nothing of a call but the allocation of its outputs.
+//
+//   CUDA      allocates the outputs and calls libtp
+//   Meta      the outputs' shapes and types
+//   Autograd  the autograd function where a gradient may be asked for; else straight on
+
+template <class F>
+auto op_of(const char* name) {
+    return c10::Dispatcher::singleton().findSchemaOrThrow((std::string("lazy_score_matrix_gb300::") + name).c_str(), "").template typed<F>();
+}
+using below_autograd = at::AutoDispatchBelowADInplaceOrView;
+
+// Whether a call on these tensors is the CUDA function's alone: no subclass, mode, trace or transform, no profiler that
+// wants to see operators. It then runs that function directly: the dispatcher's two passes add 0.3 us to the 2.1 that a call
+// takes on a Grace core without its launch, and with the launch behind them 1 to 2, a third of a short row's kernel.
+template <class... T>
+bool plain(const T&... tensors) {
+    constexpr auto ordinary = c10::DispatchKeySet({c10::DispatchKey::Dense, c10::DispatchKey::BackendSelect, c10::DispatchKey::ADInplaceOrView}) |
+                              c10::autograd_dispatch_keyset | c10::autocast_dispatch_keyset;
+    auto keys = c10::impl::tls_local_dispatch_key_set().included_;
+    const auto add = [&](const Tensor& t) {
+        keys = keys | t.key_set();
+        return t.is_cuda();
+    };
+    const bool cuda = (add(tensors) && ...);
+    return cuda && !(keys.raw_repr() & ~ordinary.raw_repr() & ~c10::full_backend_mask) && !at::getStepCallbacksUnlessEmpty(at::RecordScope::FUNCTION);
+}
+bool wants_grad(const Tensor& t) { return at::GradMode::is_enabled() && t.requires_grad(); }
 
 // --- token_logprobs ---------------------------------------------------------------------------------------------
 
 struct Logprobs {
-    Tensor logprobs, entropy, top_logprobs, top_ids, stats;
+    Tensor entropy, logprobs, top_logprobs, top_ids, stats;
+    // as the operator returns them: those that there are
+    std::vector<Tensor> list() const {
+        std::vector<Tensor> o;
+        o.reserve(5);
+        for (const Tensor* t : {&entropy, &logprobs, &top_logprobs, &top_ids, &stats})
+            if (t->defined()) o.push_back(*t);
+        return o;
+    }
 };
 
-Logprobs logprobs_forward(const Rows& x, const Tensor& tokens, double temperature, int64_t top, bool stats) {
-    const auto f32 = x.t.options().dtype(at::kFloat);
-    const auto lead = lead_of(x.t);
+Logprobs logprobs_outputs(const Tensor& logits, bool tokens, int64_t top, bool stats) {
+    check_rows_type(logits, "logits");
+    TORCH_CHECK_VALUE(top >= 0 && top <= kMaxList && top <= logits.size(-1), "top must be in [0, min(M, 128)], got ", top);
+    const auto f32 = logits.options().dtype(at::kFloat);
+    const auto lead = lead_of(logits);
     Logprobs o;
-    if (tokens.defined()) o.logprobs = at::empty(lead, f32);
+    if (tokens) o.logprobs = at::empty(lead, f32);
     o.entropy = at::empty(lead, f32);
     if (top) {
         const auto shape = with(lead, top);
         o.top_logprobs = at::empty(shape, f32);
         o.top_ids = at::empty(shape, f32.dtype(at::kLong));
     }
-    if (stats) o.stats = at::empty({x.r.N, kStats}, f32);
+    if (stats) o.stats = at::empty({logits.numel() / logits.size(-1), kStats}, f32);
+    return o;
+}
+
+Logprobs logprobs_forward(const Tensor& logits, const OptTensor& tokens_, double temperature, int64_t top, bool stats) {
+    const Rows x = rows_of(logits, "logits");
+    const Tensor tokens = side(tokens_, at::kLong, "tokens", lead_of(logits), logits);
+    const Logprobs o = logprobs_outputs(logits, tokens.defined(), top, stats);
     if (x.r.N) {
         const c10::cuda::CUDAGuard guard(x.t.device());
-        check(tp_token_logprobs(&x.r, ptr<const int64_t>(tokens), temperature, (int)top, ptr<float>(o.logprobs),
-                                ptr<float>(o.entropy), ptr<float>(o.stats), ptr<float>(o.top_logprobs),
-                                ptr<int64_t>(o.top_ids), stream_of(x.t)),
+        check(tp_token_logprobs(&x.r, ptr<const int64_t>(tokens), temperature, (int)top, ptr<float>(o.logprobs), ptr<float>(o.entropy),
+                                ptr<float>(o.stats), ptr<float>(o.top_logprobs), ptr<int64_t>(o.top_ids), stream_of(x.t)),
               "tp_token_logprobs");
     }
     return o;
 }
 
+std::vector<Tensor> logprobs_cuda(const Tensor& logits, const OptTensor& tokens, double temperature, int64_t top, bool stats) {
+    return logprobs_forward(logits, tokens, temperature, top, stats).list();
+}
+std::vector<Tensor> logprobs_meta(const Tensor& logits, const OptTensor& tokens, double, int64_t top, bool stats) {
+    return logprobs_outputs(logits, side(tokens, at::kLong, "tokens", lead_of(logits), logits).defined(), top, stats).list();
+}
+std::vector<Tensor> logprobs_op(const Tensor& logits, const OptTensor& tokens, double temperature, int64_t top, bool stats) {
+    static const auto op = op_of<decltype(logprobs_op)>("token_logprobs");
+    return op.call(logits, tokens, temperature, top, stats);
+}
+
+Tensor logprobs_backward_meta(const Tensor& logits, const OptTensor&, double, const Tensor&, const OptTensor&, const OptTensor&) {
+    return at::empty(logits.sizes(), logits.options());
+}
+
+Tensor logprobs_backward_cuda(const Tensor& logits, const OptTensor& tokens_, double temperature, const Tensor& stats_,
+                              const OptTensor& g_logprobs, const OptTensor& g_entropy) {
+    const Rows x = rows_of(logits, "logits");
+    const auto lead = lead_of(logits);
+    const Tensor tokens = side(tokens_, at::kLong, "tokens", lead, logits), stats = side(stats_, at::kFloat, "stats", {x.r.N, kStats}, logits);
+    const Tensor g_lp = side(g_logprobs, at::kFloat, "grad_logprobs", lead, logits), g_h = side(g_entropy, at::kFloat, "grad_entropy", lead, logits);
+    Tensor grad = at::empty(logits.sizes(), logits.options());
+    if (x.r.N) {
+        const c10::cuda::CUDAGuard guard(x.t.device());
+        const tp_rows g = dense(x.r, grad);
+        check(tp_token_logprobs_backward(&x.r, ptr<const int64_t>(tokens), temperature, ptr<const float>(stats), ptr<const float>(g_lp),
+                                         ptr<const float>(g_h), &g, stream_of(x.t)),
+              "tp_token_logprobs_backward");
+    }
+    return grad;
+}
+
+Tensor logprobs_backward_op(const Tensor& logits, const OptTensor& tokens, double temperature, const Tensor& stats,
+                            const OptTensor& g_logprobs, const OptTensor& g_entropy) {
+    static const auto op = op_of<decltype(logprobs_backward_op)>("token_logprobs_backward");
+    return op.call(logits, tokens, temperature, stats, g_logprobs, g_entropy);
+}
+
 struct LogprobsFn : torch::autograd::Function<LogprobsFn> {
-    // outputs: entropy, then log probabilities (with tokens), then alternatives (with top)
     static variable_list forward(torch::autograd::AutogradContext* ctx, const Tensor& logits, const Tensor& tokens,
                                  double temperature, int64_t top) {
-        const Rows x = rows_of(logits, "logits");
-        const Logprobs o = logprobs_forward(x, tokens, temperature, top, true);
+        const below_autograd guard;
+        const Tensor x = readable(logits);
+        auto out = logprobs_op(x, maybe(tokens), temperature, top, true);
         ctx->set_materialize_grads(false);
-        ctx->save_for_backward({x.t, tokens, o.stats});
+        ctx->save_for_backward({x, tokens, out.back()});
         ctx->saved_data["T"] = temperature;
-        variable_list out{o.entropy};
-        if (tokens.defined()) out.push_back(o.logprobs);
-        if (top) {
-            ctx->mark_non_differentiable({o.top_logprobs, o.top_ids});
-            out.push_back(o.top_logprobs);
-            out.push_back(o.top_ids);
-        }
+        ctx->mark_non_differentiable({out.end() - (top ? 3 : 1), out.end()});
         return out;
     }
     static variable_list backward(torch::autograd::AutogradContext* ctx, const variable_list& grads) {
         const auto saved = ctx->get_saved_variables();
-        const Tensor &tokens = saved[1], &stats = saved[2];
-        const Tensor g_h = dense_grad(grads[0]), g_lp = tokens.defined() ? dense_grad(grads[1]) : Tensor();
+        const Tensor &tokens = saved[1], &g_h = grads[0], g_lp = tokens.defined() ? grads[1] : Tensor();
         if (!g_h.defined() && !g_lp.defined()) return {Tensor(), Tensor(), Tensor(), Tensor()};
-        const Rows x = rows_of(saved[0], "logits");  // a saved tensor may come back at another address
-        Tensor grad = at::empty(x.t.sizes(), x.t.options());
-        if (x.r.N) {
-            const c10::cuda::CUDAGuard guard(x.t.device());
-            const tp_rows g = dense(x.r, grad);
-            check(tp_token_logprobs_backward(&x.r, ptr<const int64_t>(tokens), ctx->saved_data["T"].toDouble(),
-                                             ptr<const float>(stats), ptr<const float>(g_lp), ptr<const float>(g_h), &g,
-                                             stream_of(x.t)),
-                  "tp_token_logprobs_backward");
-        }
-        return {once(grad), Tensor(), Tensor(), Tensor()};
+        const auto grad = [&] {
+            const below_autograd guard;
+            return logprobs_backward_op(saved[0], maybe(tokens), ctx->saved_data["T"].toDouble(), saved[2], maybe(g_lp), maybe(g_h));
+        };
+        return {once(grad()), Tensor(), Tensor(), Tensor()};
     }
 };
 
+std::vector<Tensor> logprobs_autograd(const Tensor& logits, const OptTensor& tokens_, double temperature, int64_t top, bool stats) {
+    if (wants_grad(logits)) {
+        check_rows_type(logits, "logits");
+        auto out = LogprobsFn::apply(logits, side(tokens_, at::kLong, "tokens", lead_of(logits), logits), temperature, top);
+        if (!stats) out.pop_back();
+        return out;
+    }
+    const below_autograd guard;
+    return logprobs_op(logits, tokens_, temperature, top, stats);
+}
+
 using Four = std::tuple<OptTensor, Tensor, OptTensor, OptTensor>;
 
-OptTensor maybe(const Tensor& t) { return t.defined() ? OptTensor(t) : std::nullopt; }
-
-Four token_logprobs(const Tensor& logits, const OptTensor& tokens_, double temperature, int64_t top) {
-    Rows x = rows_of(logits, "logits");
-    TORCH_CHECK_VALUE(top >= 0 && top <= kMaxList && top <= x.r.M, "top must be in [0, min(M, 128)], got ", top);
-    const Tensor tokens = side(tokens_, at::kLong, "tokens", lead_of(logits), logits);
-    if (!(at::GradMode::is_enabled() && logits.requires_grad())) {
-        const Logprobs o = logprobs_forward(x, tokens, temperature, top, false);
+Four token_logprobs(const Tensor& logits, const OptTensor& tokens, double temperature, int64_t top) {
+    check_device(logits);
+    if (!wants_grad(logits) && (tokens ? plain(logits, *tokens) : plain(logits))) {
+        const Logprobs o = logprobs_forward(logits, tokens, temperature, top, false);
         return {maybe(o.logprobs), o.entropy, maybe(o.top_logprobs), maybe(o.top_ids)};
     }
-    const auto out = LogprobsFn::apply(logits, tokens, temperature, top);
-    const size_t at = tokens.defined() ? 2 : 1;
-    return {tokens.defined() ? OptTensor(out[1]) : std::nullopt, out[0], top ? OptTensor(out[at]) : std::nullopt,
+    const auto out = logprobs_op(logits, tokens, temperature, top, false);
+    const size_t at = tokens ? 2 : 1;
+    return {tokens ? OptTensor(out[1]) : std::nullopt, out[0], top ? OptTensor(out[at]) : std::nullopt,
             top ? OptTensor(out[at + 1]) : std::nullopt};
 }
 
@@ -220,88 +308,236 @@ Teacher teacher_of(const Tensor& ids, const Tensor& values, const Tensor& logits
                    (int)ids.size(-1)};
 }
 
-std::pair<Tensor, Tensor> distillation_forward(const Rows& x, const Teacher& y, double temperature, bool rest, bool want_stats) {
-    const auto f32 = x.t.options().dtype(at::kFloat);
-    Tensor loss = at::empty(lead_of(x.t), f32), stats = want_stats ? at::empty({x.r.N, kStats}, f32) : Tensor();
+struct Distillation {
+    Tensor loss, stats;
+    std::vector<Tensor> list() const { return stats.defined() ? std::vector<Tensor>{loss, stats} : std::vector<Tensor>{loss}; }
+};
+
+Distillation distillation_outputs(const Tensor& logits, bool stats) {
+    check_rows_type(logits, "logits");
+    const auto f32 = logits.options().dtype(at::kFloat);
+    return {at::empty(lead_of(logits), f32), stats ? at::empty({logits.numel() / logits.size(-1), kStats}, f32) : Tensor()};
+}
+
+Distillation distillation_forward(const Tensor& logits, const Tensor& ids, const Tensor& values, double temperature, bool rest, bool stats) {
+    const Rows x = rows_of(logits, "logits");
+    const Teacher y = teacher_of(ids, values, logits);
+    const Distillation o = distillation_outputs(logits, stats);
     if (x.r.N) {
         const c10::cuda::CUDAGuard guard(x.t.device());
         check(tp_topk_distillation(&x.r, y.K, ptr<const int64_t>(y.ids), ptr<const float>(y.values), temperature, rest,
-                                   ptr<float>(loss), ptr<float>(stats), stream_of(x.t)),
+                                   ptr<float>(o.loss), ptr<float>(o.stats), stream_of(x.t)),
               "tp_topk_distillation");
     }
-    return {loss, stats};
+    return o;
+}
+
+std::vector<Tensor> distillation_cuda(const Tensor& logits, const Tensor& ids, const Tensor& values, double temperature, bool rest,
+                                      bool stats) {
+    return distillation_forward(logits, ids, values, temperature, rest, stats).list();
+}
+std::vector<Tensor> distillation_meta(const Tensor& logits, const Tensor& ids, const Tensor& values, double, bool, bool stats) {
+    const Distillation o = distillation_outputs(logits, stats);
+    teacher_of(ids, values, logits);
+    return o.list();
+}
+std::vector<Tensor> distillation_op(const Tensor& logits, const Tensor& ids, const Tensor& values, double temperature, bool rest,
+                                    bool stats) {
+    static const auto op = op_of<decltype(distillation_op)>("topk_distillation");
+    return op.call(logits, ids, values, temperature, rest, stats);
+}
+
+Tensor distillation_backward_meta(const Tensor& logits, const Tensor&, const Tensor&, double, bool, const Tensor&, const Tensor&) {
+    return at::empty(logits.sizes(), logits.options());
+}
+
+Tensor distillation_backward_cuda(const Tensor& logits, const Tensor& ids, const Tensor& values, double temperature, bool rest,
+                                  const Tensor& stats_, const Tensor& g_loss) {
+    const Rows x = rows_of(logits, "logits");
+    const Teacher y = teacher_of(ids, values, logits);
+    const Tensor stats = side(stats_, at::kFloat, "stats", {x.r.N, kStats}, logits), g = side(g_loss, at::kFloat, "grad_loss", lead_of(logits), logits);
+    Tensor grad = at::empty(logits.sizes(), logits.options());
+    if (x.r.N) {
+        const c10::cuda::CUDAGuard guard(x.t.device());
+        const tp_rows rows = dense(x.r, grad);
+        check(tp_topk_distillation_backward(&x.r, y.K, ptr<const int64_t>(y.ids), ptr<const float>(y.values), temperature, rest,
+                                            ptr<const float>(stats), ptr<const float>(g), &rows, stream_of(x.t)),
+              "tp_topk_distillation_backward");
+    }
+    return grad;
+}
+
+Tensor distillation_backward_op(const Tensor& logits, const Tensor& ids, const Tensor& values, double temperature, bool rest,
+                                const Tensor& stats, const Tensor& g_loss) {
+    static const auto op = op_of<decltype(distillation_backward_op)>("topk_distillation_backward");
+    return op.call(logits, ids, values, temperature, rest, stats, g_loss);
 }
 
 struct DistillationFn : torch::autograd::Function<DistillationFn> {
-    static Tensor forward(torch::autograd::AutogradContext* ctx, const Tensor& logits, const Tensor& ids, const Tensor& values,
-                          double temperature, bool rest) {
-        const Rows x = rows_of(logits, "logits");
-        const auto [loss, stats] = distillation_forward(x, Teacher{ids, values, (int)ids.size(-1)}, temperature, rest, true);
-        ctx->save_for_backward({x.t, ids, values, stats});
+    static variable_list forward(torch::autograd::AutogradContext* ctx, const Tensor& logits, const Tensor& ids, const Tensor& values,
+                                 double temperature, bool rest) {
+        const below_autograd guard;
+        const Tensor x = readable(logits);
+        auto out = distillation_op(x, ids, values, temperature, rest, true);
+        ctx->set_materialize_grads(false);
+        ctx->save_for_backward({x, ids, values, out[1]});
         ctx->saved_data["T"] = temperature;
         ctx->saved_data["rest"] = rest;
-        return loss;
+        ctx->mark_non_differentiable({out[1]});
+        return out;
     }
     static variable_list backward(torch::autograd::AutogradContext* ctx, const variable_list& grads) {
         const auto saved = ctx->get_saved_variables();
-        const Rows x = rows_of(saved[0], "logits");
-        const Tensor g_loss = dense_grad(grads[0]);
-        Tensor grad = at::empty(x.t.sizes(), x.t.options());
-        if (x.r.N) {
-            const c10::cuda::CUDAGuard guard(x.t.device());
-            const tp_rows g = dense(x.r, grad);
-            check(tp_topk_distillation_backward(&x.r, (int)saved[1].size(-1), ptr<const int64_t>(saved[1]),
-                                                ptr<const float>(saved[2]), ctx->saved_data["T"].toDouble(),
-                                                ctx->saved_data["rest"].toBool(), ptr<const float>(saved[3]),
-                                                ptr<const float>(g_loss), &g, stream_of(x.t)),
-                  "tp_topk_distillation_backward");
-        }
-        return {once(grad), Tensor(), Tensor(), Tensor(), Tensor()};
+        if (!grads[0].defined()) return {Tensor(), Tensor(), Tensor(), Tensor(), Tensor()};
+        const auto grad = [&] {
+            const below_autograd guard;
+            return distillation_backward_op(saved[0], saved[1], saved[2], ctx->saved_data["T"].toDouble(), ctx->saved_data["rest"].toBool(),
+                                            saved[3], grads[0]);
+        };
+        return {once(grad()), Tensor(), Tensor(), Tensor(), Tensor()};
     }
 };
 
+std::vector<Tensor> distillation_autograd(const Tensor& logits, const Tensor& ids, const Tensor& values, double temperature, bool rest,
+                                          bool stats) {
+    TORCH_CHECK_VALUE(!wants_grad(values), "topk_distillation: the teacher's list is a constant; pass teacher_values.detach()");
+    if (wants_grad(logits)) {
+        check_rows_type(logits, "logits");
+        const Teacher y = teacher_of(ids, values, logits);
+        auto out = DistillationFn::apply(logits, y.ids, y.values, temperature, rest);
+        if (!stats) out.pop_back();
+        return out;
+    }
+    const below_autograd guard;
+    return distillation_op(logits, ids, values, temperature, rest, stats);
+}
+
 Tensor topk_distillation(const Tensor& logits, const Tensor& ids, const Tensor& values, double temperature, bool rest) {
-    const Rows x = rows_of(logits, "logits");
-    const bool grad = at::GradMode::is_enabled();
-    TORCH_CHECK_VALUE(!(grad && values.requires_grad()),
-                      "topk_distillation: the teacher's list is a constant; pass teacher_values.detach()");
+    check_device(logits);
+    if (!wants_grad(logits) && !wants_grad(values) && plain(logits, ids, values))
+        return distillation_forward(logits, ids, values, temperature, rest, false).loss;
+    return distillation_op(logits, ids, values, temperature, rest, false)[0];
+}
+
+// The loss, and its gradient into `grad` (rows g).
+Tensor distillation_grad_into(const Rows& x, const Tensor& logits, const Tensor& ids, const Tensor& values, const OptTensor& weights,
+                              double temperature, bool rest, const tp_rows& g) {
     const Teacher y = teacher_of(ids, values, logits);
-    if (grad && logits.requires_grad()) return DistillationFn::apply(logits, y.ids, y.values, temperature, rest);
-    return distillation_forward(x, y, temperature, rest, false).first;
+    const Tensor w = side(weights, at::kFloat, "weights", lead_of(logits), logits);
+    const Distillation o = distillation_outputs(logits, true);
+    if (x.r.N) {
+        const c10::cuda::CUDAGuard guard(x.t.device());
+        check(tp_topk_distillation_grad(&x.r, y.K, ptr<const int64_t>(y.ids), ptr<const float>(y.values), ptr<const float>(w),
+                                        temperature, rest, ptr<float>(o.loss), ptr<float>(o.stats), &g, stream_of(x.t)),
+              "tp_topk_distillation_grad");
+    }
+    return o.loss;
+}
+
+std::tuple<Tensor, Tensor> distillation_grad_meta(const Tensor& logits, const Tensor& ids, const Tensor& values, const OptTensor& weights,
+                                                  double, bool) {
+    const Tensor loss = distillation_outputs(logits, false).loss;
+    teacher_of(ids, values, logits);
+    side(weights, at::kFloat, "weights", lead_of(logits), logits);
+    return {loss, at::empty(logits.sizes(), logits.options())};
+}
+std::tuple<Tensor, Tensor> distillation_grad_cuda(const Tensor& logits, const Tensor& ids, const Tensor& values, const OptTensor& weights,
+                                                  double temperature, bool rest) {
+    const Rows x = rows_of(logits, "logits");
+    const Tensor grad = at::empty(logits.sizes(), logits.options());
+    return {distillation_grad_into(x, logits, ids, values, weights, temperature, rest, dense(x.r, grad)), grad};
+}
+std::tuple<Tensor, Tensor> distillation_grad_op(const Tensor& logits, const Tensor& ids, const Tensor& values, const OptTensor& weights,
+                                                double temperature, bool rest) {
+    static const auto op = op_of<decltype(distillation_grad_op)>("topk_distillation_grad");
+    return op.call(logits, ids, values, weights, temperature, rest);
+}
+std::tuple<Tensor, Tensor> distillation_grad_autograd(const Tensor& logits, const Tensor& ids, const Tensor& values,
+                                                      const OptTensor& weights, double temperature, bool rest) {
+    const below_autograd guard;
+    return distillation_grad_op(logits, ids, values, weights, temperature, rest);
+}
+
+void check_out(const Tensor& logits, const Tensor& out) {
+    TORCH_CHECK_VALUE(out.sizes() == logits.sizes() && out.scalar_type() == logits.scalar_type() && out.device() == logits.device(),
+                      "out must have the logits' shape, dtype and device");
+}
+Tensor distillation_grad_out_meta(const Tensor& logits, const Tensor& ids, const Tensor& values, const OptTensor& weights, double,
+                                  bool, Tensor& out) {
+    check_out(logits, out);
+    return std::get<0>(distillation_grad_meta(logits, ids, values, weights, 1.0, false));
+}
+Tensor distillation_grad_out_cuda(const Tensor& logits, const Tensor& ids, const Tensor& values, const OptTensor& weights,
+                                  double temperature, bool rest, Tensor& out) {
+    const Rows x = rows_of(logits, "logits");
+    check_out(logits, out);
+    const Tensor loss = distillation_grad_into(x, logits, ids, values, weights, temperature, rest, rows_of(out, "out", /*copy=*/false).r);
+    torch::autograd::impl::bump_version(out);  // a graph that saved it must not use it any more
+    return loss;
+}
+Tensor distillation_grad_out_op(const Tensor& logits, const Tensor& ids, const Tensor& values, const OptTensor& weights,
+                                double temperature, bool rest, Tensor& out) {
+    static const auto op = op_of<decltype(distillation_grad_out_op)>("topk_distillation_grad_out");
+    return op.call(logits, ids, values, weights, temperature, rest, out);
+}
+Tensor distillation_grad_out_autograd(const Tensor& logits, const Tensor& ids, const Tensor& values, const OptTensor& weights,
+                                      double temperature, bool rest, Tensor& out) {
+    const below_autograd guard;
+    return distillation_grad_out_op(logits, ids, values, weights, temperature, rest, out);
 }
 
 std::tuple<Tensor, Tensor> topk_distillation_grad(const Tensor& logits, const Tensor& ids, const Tensor& values,
                                                   const OptTensor& weights, double temperature, bool rest,
                                                   const OptTensor& out) {
+    check_device(logits);
     const at::NoGradGuard no_grad;
-    const Rows x = rows_of(logits, "logits");
-    const Teacher y = teacher_of(ids, values, logits);
-    const Tensor w = side(weights, at::kFloat, "weights", lead_of(logits), logits);
-    const auto f32 = x.t.options().dtype(at::kFloat);
-    Tensor grad;
-    tp_rows g;
-    if (out) {
-        grad = *out;
-        TORCH_CHECK_VALUE(grad.sizes() == logits.sizes() && grad.scalar_type() == logits.scalar_type() &&
-                              grad.device() == logits.device(),
-                          "out must have the logits' shape, dtype and device");
-        g = rows_of(grad, "out", /*copy=*/false).r;
-    } else {
-        grad = at::empty(x.t.sizes(), x.t.options());
-        g = dense(x.r, grad);
+    const bool direct = weights ? plain(logits, ids, values, *weights) : plain(logits, ids, values);
+    if (!out) {
+        if (direct) return distillation_grad_cuda(logits, ids, values, weights, temperature, rest);
+        return distillation_grad_op(logits, ids, values, weights, temperature, rest);
     }
-    Tensor loss = at::empty(lead_of(x.t), f32), stats = at::empty({x.r.N, kStats}, f32);
-    if (x.r.N) {
-        const c10::cuda::CUDAGuard guard(x.t.device());
-        check(tp_topk_distillation_grad(&x.r, y.K, ptr<const int64_t>(y.ids), ptr<const float>(y.values), ptr<const float>(w),
-                                        temperature, rest, ptr<float>(loss), ptr<float>(stats), &g, stream_of(x.t)),
-              "tp_topk_distillation_grad");
-    }
-    if (out) torch::autograd::impl::bump_version(grad);  // a graph that saved it must not use it any more
+    Tensor grad = *out;
+    const Tensor loss = direct && plain(grad) ? distillation_grad_out_cuda(logits, ids, values, weights, temperature, rest, grad)
+                                              : distillation_grad_out_op(logits, ids, values, weights, temperature, rest, grad);
     return {loss, grad};
 }
 
 }  // namespace
+
+TORCH_LIBRARY(lazy_score_matrix_gb300, m) {
+    m.def("token_logprobs(Tensor logits, Tensor? tokens, float temperature, int top, bool stats) -> Tensor[]");
+    m.def("token_logprobs_backward(Tensor logits, Tensor? tokens, float temperature, Tensor stats, Tensor? grad_logprobs, "
+          "Tensor? grad_entropy) -> Tensor");
+    m.def("topk_distillation(Tensor logits, Tensor ids, Tensor values, float temperature, bool rest, bool stats) -> Tensor[]");
+    m.def("topk_distillation_backward(Tensor logits, Tensor ids, Tensor values, float temperature, bool rest, Tensor stats, "
+          "Tensor grad_loss) -> Tensor");
+    m.def("topk_distillation_grad(Tensor logits, Tensor ids, Tensor values, Tensor? weights, float temperature, bool rest) -> "
+          "(Tensor, Tensor)");
+    m.def("topk_distillation_grad_out(Tensor logits, Tensor ids, Tensor values, Tensor? weights, float temperature, bool rest, "
+          "Tensor(a!) out) -> Tensor");
+}
+TORCH_LIBRARY_IMPL(lazy_score_matrix_gb300, CUDA, m) {
+    m.impl("token_logprobs", &logprobs_cuda);
+    m.impl("token_logprobs_backward", &logprobs_backward_cuda);
+    m.impl("topk_distillation", &distillation_cuda);
+    m.impl("topk_distillation_backward", &distillation_backward_cuda);
+    m.impl("topk_distillation_grad", &distillation_grad_cuda);
+    m.impl("topk_distillation_grad_out", &distillation_grad_out_cuda);
+}
+TORCH_LIBRARY_IMPL(lazy_score_matrix_gb300, Meta, m) {
+    m.impl("token_logprobs", &logprobs_meta);
+    m.impl("token_logprobs_backward", &logprobs_backward_meta);
+    m.impl("topk_distillation", &distillation_meta);
+    m.impl("topk_distillation_backward", &distillation_backward_meta);
+    m.impl("topk_distillation_grad", &distillation_grad_meta);
+    m.impl("topk_distillation_grad_out", &distillation_grad_out_meta);
+}
+TORCH_LIBRARY_IMPL(lazy_score_matrix_gb300, Autograd, m) {
+    m.impl("token_logprobs", &logprobs_autograd);
+    m.impl("topk_distillation", &distillation_autograd);
+    m.impl("topk_distillation_grad", &distillation_grad_autograd);
+    m.impl("topk_distillation_grad_out", &distillation_grad_out_autograd);
+}
 
 PYBIND11_MODULE(_tp_logits, m) {
     m.def("token_logprobs", &token_logprobs);

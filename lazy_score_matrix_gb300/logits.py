@@ -13,6 +13,10 @@ Logits are float32, float16 or bfloat16 CUDA tensors of any leading shape; rows 
 a padded vocabulary, ``logits[:, :-1]`` of a batch) and are copied only when two strides cannot describe them.
 Results are float32, gradients have the logits' type. Columns at -inf are masked: probability 0, never chosen.
 
+The calls are operators of PyTorch's dispatcher: a trace (``torch.jit.trace``, ``make_fx``) holds them, runs them again
+on its own inputs and has their gradients. (A trace saved to a file needs ``_lib.logits_binding()`` before it is
+loaded: the operators are registered with the binding.)
+
 Under CUDA graph capture, call these as anywhere else: they allocate outputs from PyTorch's allocator and use no
 workspace. For a captured backward use leaves of their own (PyTorch ties a leaf to the stream it was first used
 on), or ``topk_distillation_grad``, which needs no autograd.

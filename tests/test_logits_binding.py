@@ -1,0 +1,139 @@
+"""What PyTorch's machinery around a call does with the stored-row consumers: tracing, function transforms, saved tensors
+that come back otherwise."""
+import pytest
+import torch
+from torch.fx.experimental.proxy_tensor import make_fx
+
+import lazy_score_matrix_gb300 as tp
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def inputs(seed, n=6, m=901, k=7, dtype=torch.float32):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x = (torch.randn(n, m, device=DEV, generator=g) * 3).to(dtype)
+    tokens = torch.randint(0, m, (n,), device=DEV, generator=g)
+    y = torch.log_softmax(x.float() + torch.randn(n, m, device=DEV, generator=g), 1)
+    values, ids = y.topk(k, 1)
+    return x, tokens, ids, values, torch.rand(n, device=DEV, generator=g) + 0.5
+
+
+def no_grad_calls(x, tokens, ids, values, w):
+    r = tp.token_logprobs(x, tokens, temperature=0.8, top=5)
+    only = tp.token_logprobs(x)
+    loss, grad = tp.topk_distillation_grad(x, ids, values, w, rest=True)
+    return (r.logprobs, r.entropy, r.top_logprobs, r.top_ids, only.entropy, tp.topk_distillation(x, ids, values), loss, grad)
+
+
+def in_place(x, tokens, ids, values, w):
+    y = x * 1.0
+    loss, grad = tp.topk_distillation_grad(y, ids, values, w, out=y)
+    return loss, grad, y
+
+
+def differentiable(x, tokens, ids, values, w):
+    r = tp.token_logprobs(x, tokens)
+    return (r.logprobs * w).sum() + 0.1 * r.entropy.sum() + (tp.topk_distillation(x, ids, values, rest=True) * w).sum()
+
+
+def traced_by_jit(f, args):
+    return torch.jit.trace(f, args, check_trace=False)
+
+
+def traced_by_fx(f, args):
+    return make_fx(f)(*args)
+
+
+TRACERS = {"jit": traced_by_jit, "fx": traced_by_fx}
+
+
+@pytest.mark.parametrize("tracer", TRACERS)
+@pytest.mark.parametrize("calls", [no_grad_calls, in_place])
+def test_traced_calls_run_again(tracer, calls):
+    traced = TRACERS[tracer](calls, inputs(1))
+    for seed in (1, 2, 3):
+        want = calls(*inputs(seed))
+        keep = [torch.randn(6, 901, device=DEV) for _ in range(4)]  # other values in the freed blocks
+        got = traced(*inputs(seed))
+        assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(got, want))
+        del keep
+
+
+def test_gradients_of_a_traced_call():
+    x, *rest = inputs(1)
+    traced = traced_by_jit(differentiable, (x.requires_grad_(True), *rest))
+    for seed in (1, 2):
+        y, *rest = inputs(seed)
+        leaves = [y.clone().requires_grad_(True) for _ in range(2)]
+        got, want = traced(leaves[0], *rest), differentiable(leaves[1], *rest)
+        assert torch.equal(got, want)
+        got.backward()
+        want.backward()
+        assert torch.equal(leaves[0].grad, leaves[1].grad)
+
+
+def test_a_traced_gradient():
+    # the whole step, its backward included, as a graph of operators
+    def step(x, *rest):
+        y = x.detach().requires_grad_(True)
+        return torch.autograd.grad(differentiable(y, *rest), y)[0]
+
+    traced = make_fx(step)(*inputs(1))
+    for seed in (1, 2):
+        assert torch.equal(traced(*inputs(seed)), step(*inputs(seed)))
+
+
+def test_traced_under_inference_mode_and_reduced_types():
+    with torch.inference_mode():
+        traced = traced_by_jit(no_grad_calls, inputs(1, dtype=torch.bfloat16))
+        args = inputs(2, dtype=torch.bfloat16)
+        assert all(torch.equal(a, b) for a, b in zip(traced(*args), no_grad_calls(*args)))
+
+
+def test_shapes_without_data():
+    # fake tensors: shapes and types of every result, nothing launched
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    args = inputs(1, dtype=torch.float16)
+    want = no_grad_calls(*args)
+    with FakeTensorMode() as mode:
+        got = no_grad_calls(*(mode.from_tensor(t) for t in args))
+    assert [(t.shape, t.dtype, t.device.type) for t in got] == [(t.shape, t.dtype, "cuda") for t in want]
+
+
+def test_function_transforms_are_right_or_refused():
+    x, tokens, ids, values, w = inputs(1)
+    calls = [(lambda: torch.vmap(lambda a, t: tp.token_logprobs(a, t).logprobs)(x, tokens), lambda: tp.token_logprobs(x, tokens).logprobs),
+             (lambda: torch.vmap(lambda a, i, v: tp.topk_distillation(a, i, v))(x, ids, values), lambda: tp.topk_distillation(x, ids, values)),
+             (lambda: torch.func.grad(lambda a: tp.token_logprobs(a, tokens).entropy.sum())(x),
+              lambda: torch.autograd.grad(tp.token_logprobs(y, tokens).entropy.sum(), y)[0])]
+    y = x.detach().requires_grad_(True)
+    for transform, plain in calls:
+        try:
+            got = transform()
+        except (NotImplementedError, RuntimeError):
+            continue
+        assert (got - plain()).abs().max() < 1e-5
+
+
+def test_saved_tensors_in_another_layout():
+    # hooks that bring a saved tensor back with other strides
+    x, tokens, ids, values, w = inputs(1, n=12)
+    x, tokens, ids, values, w = x.view(3, 4, -1), tokens.view(3, 4), ids.view(3, 4, -1), values.view(3, 4, -1), w.view(3, 4)
+
+    def grad():
+        leaf = x.detach().requires_grad_(True)
+        return torch.autograd.grad(differentiable(leaf, tokens, ids, values, w), leaf)[0]
+
+    want = grad()
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: t, lambda t: t.transpose(0, -1).contiguous().transpose(0, -1)):
+        got = grad()
+    assert torch.equal(got, want)
+
+
+def test_negated_views():
+    # a view that PyTorch negates when it is read
+    x, tokens, ids, values, w = inputs(1, n=1)
+    neg = torch.complex(torch.zeros_like(w), -w).conj().imag
+    assert neg.is_neg() and torch.equal(neg, w)
+    assert torch.equal(tp.topk_distillation_grad(x, ids, values, neg)[1], tp.topk_distillation_grad(x, ids, values, w)[1])
