@@ -245,13 +245,14 @@ Tensor logprobs_backward_op(const Tensor& logits, const OptTensor& tokens, doubl
 }
 
 struct LogprobsFn : torch::autograd::Function<LogprobsFn> {
-    static variable_list forward(torch::autograd::AutogradContext* ctx, const Tensor& logits, const Tensor& tokens,
+    // tokens as an optional: autograd takes a Tensor argument for one that is defined
+    static variable_list forward(torch::autograd::AutogradContext* ctx, const Tensor& logits, const OptTensor& tokens,
                                  double temperature, int64_t top) {
         const below_autograd guard;
         const Tensor x = readable(logits);
-        auto out = logprobs_op(x, maybe(tokens), temperature, top, true);
+        auto out = logprobs_op(x, tokens, temperature, top, true);
         ctx->set_materialize_grads(false);
-        ctx->save_for_backward({x, tokens, out.back()});
+        ctx->save_for_backward({x, tokens ? *tokens : Tensor(), out.back()});
         ctx->saved_data["T"] = temperature;
         ctx->mark_non_differentiable({out.end() - (top ? 3 : 1), out.end()});
         return out;
@@ -271,7 +272,7 @@ struct LogprobsFn : torch::autograd::Function<LogprobsFn> {
 std::vector<Tensor> logprobs_autograd(const Tensor& logits, const OptTensor& tokens_, double temperature, int64_t top, bool stats) {
     if (wants_grad(logits)) {
         check_rows_type(logits, "logits");
-        auto out = LogprobsFn::apply(logits, side(tokens_, at::kLong, "tokens", lead_of(logits), logits), temperature, top);
+        auto out = LogprobsFn::apply(logits, maybe(side(tokens_, at::kLong, "tokens", lead_of(logits), logits)), temperature, top);
         if (!stats) out.pop_back();
         return out;
     }

@@ -5,6 +5,7 @@ import torch
 from torch.fx.experimental.proxy_tensor import make_fx
 
 import lazy_score_matrix_gb300 as tp
+from tests.test_logits import check_logprobs, scores
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -137,3 +138,18 @@ def test_negated_views():
     neg = torch.complex(torch.zeros_like(w), -w).conj().imag
     assert neg.is_neg() and torch.equal(neg, w)
     assert torch.equal(tp.topk_distillation_grad(x, ids, values, neg)[1], tp.topk_distillation_grad(x, ids, values, w)[1])
+
+
+@pytest.mark.parametrize("n,m", [(3, 2), (5, 261), (4, 20011), (1300, 700)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("top", [0, 2])
+def test_entropy_and_its_gradient_without_tokens(n, m, dtype, top):
+    x = scores(min(n, 6), m, dtype, m).repeat((n + 5) // 6, 1)[:n]
+    check_logprobs(x[:6], None, 0.9, top)
+    leaves = [x.to(DEV).requires_grad_(True) for _ in range(2)]
+    # the same alternatives on both sides: with and without them a row's sums are split over other threads
+    r = tp.token_logprobs(leaves[0], temperature=0.9, top=top)
+    w = tp.token_logprobs(leaves[1], torch.zeros(n, dtype=torch.int64, device=DEV), temperature=0.9, top=top)
+    assert r.logprobs is None and torch.equal(r.entropy, w.entropy)
+    grads = [torch.autograd.grad(o.entropy.sum(), leaf)[0] for o, leaf in zip((r, w), leaves)]
+    assert torch.equal(*grads)
