@@ -143,10 +143,19 @@ template <class F>
 auto op_of(const char* name) {
     return c10::Dispatcher::singleton().findSchemaOrThrow((std::string("lazy_score_matrix_gb300::") + name).c_str(), "").template typed<F>();
 }
+
+// No forward-mode derivatives, as the lazy consumers have none: a tangent is refused, not dropped.
+bool tangent(const Tensor& t) { return t.defined() && t._fw_grad(/*level=*/0).defined(); }
+bool tangent(const OptTensor& t) { return t && tangent(*t); }
+template <class... T>
+void refuse_tangents(const char* where, const T&... tensors) {
+    TORCH_CHECK_NOT_IMPLEMENTED(!(tangent(tensors) || ...), where, ": no forward-mode derivative; libtp has reverse mode only");
+}
+
 using below_autograd = at::AutoDispatchBelowADInplaceOrView;
 
-// Whether a call on these tensors is the CUDA function's alone: no subclass, mode, trace or transform, no profiler that
-// wants to see operators. It then runs that function directly: the dispatcher's two passes add 0.3 us to the 2.1 that a call
+// Whether a call on these tensors is the CUDA function's alone: no subclass, mode, trace or transform, no tangent, no
+// profiler that wants to see operators. It then runs that function directly: the dispatcher's two passes add 0.3 us to the 2.1 that a call
 // takes on a Grace core without its launch, and with the launch behind them 1 to 2, a third of a short row's kernel.
 template <class... T>
 bool plain(const T&... tensors) {
@@ -155,7 +164,7 @@ bool plain(const T&... tensors) {
     auto keys = c10::impl::tls_local_dispatch_key_set().included_;
     const auto add = [&](const Tensor& t) {
         keys = keys | t.key_set();
-        return t.is_cuda();
+        return t.is_cuda() && !tangent(t);
     };
     const bool cuda = (add(tensors) && ...);
     return cuda && !(keys.raw_repr() & ~ordinary.raw_repr() & ~c10::full_backend_mask) && !at::getStepCallbacksUnlessEmpty(at::RecordScope::FUNCTION);
@@ -260,6 +269,7 @@ struct LogprobsFn : torch::autograd::Function<LogprobsFn> {
     static variable_list backward(torch::autograd::AutogradContext* ctx, const variable_list& grads) {
         const auto saved = ctx->get_saved_variables();
         const Tensor &tokens = saved[1], &g_h = grads[0], g_lp = tokens.defined() ? grads[1] : Tensor();
+        refuse_tangents("token_logprobs", g_h, g_lp);
         if (!g_h.defined() && !g_lp.defined()) return {Tensor(), Tensor(), Tensor(), Tensor()};
         const auto grad = [&] {
             const below_autograd guard;
@@ -270,6 +280,7 @@ struct LogprobsFn : torch::autograd::Function<LogprobsFn> {
 };
 
 std::vector<Tensor> logprobs_autograd(const Tensor& logits, const OptTensor& tokens_, double temperature, int64_t top, bool stats) {
+    refuse_tangents("token_logprobs", logits);
     if (wants_grad(logits)) {
         check_rows_type(logits, "logits");
         auto out = LogprobsFn::apply(logits, maybe(side(tokens_, at::kLong, "tokens", lead_of(logits), logits)), temperature, top);
@@ -389,6 +400,7 @@ struct DistillationFn : torch::autograd::Function<DistillationFn> {
     }
     static variable_list backward(torch::autograd::AutogradContext* ctx, const variable_list& grads) {
         const auto saved = ctx->get_saved_variables();
+        refuse_tangents("topk_distillation", grads[0]);
         if (!grads[0].defined()) return {Tensor(), Tensor(), Tensor(), Tensor(), Tensor()};
         const auto grad = [&] {
             const below_autograd guard;
@@ -401,6 +413,7 @@ struct DistillationFn : torch::autograd::Function<DistillationFn> {
 
 std::vector<Tensor> distillation_autograd(const Tensor& logits, const Tensor& ids, const Tensor& values, double temperature, bool rest,
                                           bool stats) {
+    refuse_tangents("topk_distillation", logits, values);
     TORCH_CHECK_VALUE(!wants_grad(values), "topk_distillation: the teacher's list is a constant; pass teacher_values.detach()");
     if (wants_grad(logits)) {
         check_rows_type(logits, "logits");
@@ -455,6 +468,7 @@ std::tuple<Tensor, Tensor> distillation_grad_op(const Tensor& logits, const Tens
 }
 std::tuple<Tensor, Tensor> distillation_grad_autograd(const Tensor& logits, const Tensor& ids, const Tensor& values,
                                                       const OptTensor& weights, double temperature, bool rest) {
+    refuse_tangents("topk_distillation_grad", logits, values, weights);
     const below_autograd guard;
     return distillation_grad_op(logits, ids, values, weights, temperature, rest);
 }
@@ -483,6 +497,7 @@ Tensor distillation_grad_out_op(const Tensor& logits, const Tensor& ids, const T
 }
 Tensor distillation_grad_out_autograd(const Tensor& logits, const Tensor& ids, const Tensor& values, const OptTensor& weights,
                                       double temperature, bool rest, Tensor& out) {
+    refuse_tangents("topk_distillation_grad", logits, values, weights, out);
     const below_autograd guard;
     return distillation_grad_out_op(logits, ids, values, weights, temperature, rest, out);
 }

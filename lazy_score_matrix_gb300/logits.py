@@ -15,7 +15,8 @@ Results are float32, gradients have the logits' type. Columns at -inf are masked
 
 The calls are operators of PyTorch's dispatcher: a trace (``torch.jit.trace``, ``make_fx``) holds them, runs them again
 on its own inputs and has their gradients. (A trace saved to a file needs ``_lib.logits_binding()`` before it is
-loaded: the operators are registered with the binding.)
+loaded: the operators are registered with the binding.) Derivatives are reverse mode, once:
+forward-mode tangents and second derivatives are refused.
 
 Under CUDA graph capture, call these as anywhere else: they allocate outputs from PyTorch's allocator and use no
 workspace. For a captured backward use leaves of their own (PyTorch ties a leaf to the stream it was first used

@@ -1,7 +1,8 @@
-"""What PyTorch's machinery around a call does with the stored-row consumers: tracing, function transforms, saved tensors
-that come back otherwise."""
+"""What PyTorch's machinery around a call does with the stored-row consumers: tracing, forward-mode derivatives, function
+transforms, saved tensors that come back otherwise."""
 import pytest
 import torch
+from torch.autograd import forward_ad
 from torch.fx.experimental.proxy_tensor import make_fx
 
 import lazy_score_matrix_gb300 as tp
@@ -100,6 +101,32 @@ def test_shapes_without_data():
     with FakeTensorMode() as mode:
         got = no_grad_calls(*(mode.from_tensor(t) for t in args))
     assert [(t.shape, t.dtype, t.device.type) for t in got] == [(t.shape, t.dtype, "cuda") for t in want]
+
+
+def test_forward_mode_is_refused():
+    x, tokens, ids, values, w = inputs(1)
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(x, torch.ones_like(x))
+        dual_values, dual_w = forward_ad.make_dual(values, torch.ones_like(values)), forward_ad.make_dual(w, torch.ones_like(w))
+        calls = [lambda: tp.token_logprobs(dual, tokens), lambda: tp.token_logprobs(dual, top=3), lambda: tp.topk_distillation(dual, ids, values),
+                 lambda: tp.topk_distillation(x, ids, dual_values), lambda: tp.topk_distillation_grad(dual, ids, values, w),
+                 lambda: tp.topk_distillation_grad(x, ids, dual_values, w), lambda: tp.topk_distillation_grad(x, ids, values, dual_w),
+                 lambda: tp.topk_distillation_grad(x, ids, values, w, out=dual)]
+        for i, call in enumerate(calls):
+            with pytest.raises(NotImplementedError):
+                call()
+                pytest.fail(f"call {i} was accepted")
+            with pytest.raises(NotImplementedError), torch.no_grad():
+                call()
+                pytest.fail(f"call {i} was accepted under no_grad")
+        # a tangent of an upstream gradient, on the way back
+        leaf = x.detach().requires_grad_(True)
+        for out in (tp.token_logprobs(leaf, tokens).logprobs, tp.token_logprobs(leaf).entropy, tp.topk_distillation(leaf, ids, values)):
+            with pytest.raises(NotImplementedError):
+                torch.autograd.grad(out, leaf, dual_w)
+    with pytest.raises((NotImplementedError, RuntimeError)):
+        torch.func.jvp(lambda t: tp.token_logprobs(t, tokens).logprobs, (x,), (torch.ones_like(x),))
+    assert torch.isfinite(tp.token_logprobs(x, tokens).logprobs).all()
 
 
 def test_function_transforms_are_right_or_refused():
