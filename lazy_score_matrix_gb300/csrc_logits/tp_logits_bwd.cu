@@ -40,7 +40,8 @@ __global__ void __launch_bounds__(kThreads) logprobs_bwd_kernel(const LogprobArg
 #pragma unroll
         for (int i = 0; i < Elem<T>::kVec; ++i) {
             float t = fmaf(f[i] - m, c, -ls2);  // log2 p
-            if (ENTROPY) t = max_nan(t, -1e30f);  // p = 0 times a finite log
+            // p = 0 from -126 on: times a small number, so that the weights' product with it stays finite up to 2^120
+            if (ENTROPY) t = max_nan(t, -128.f);
             f[i] = -ex2(t) * (ENTROPY ? fmaf(b2, t, b1) : g1);
         }
         if (tok >= e && tok < e + Elem<T>::kVec) {

@@ -1,5 +1,5 @@
-"""Stored score rows at the ends of fp32's range: columns masked by the type's lowest value at any temperature.
-Against the 64-bit forms of _rows_ref.py."""
+"""Stored score rows at the ends of fp32's range: columns masked by the type's lowest value at any temperature, and
+upstream gradients far above one. Against the 64-bit forms of _rows_ref.py."""
 import math
 
 import pytest
@@ -95,3 +95,24 @@ def test_infinite_and_nan_scores_still_show(rest):
     for loss in (tp.topk_distillation(x, ids, values, temperature=0.7, rest=rest),
                  tp.topk_distillation_grad(x, ids, values, temperature=0.7, rest=rest)[0]):
         assert loss.isnan().tolist() == [True, True, True, False]
+
+
+@pytest.mark.parametrize("n,m", SHAPES)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,g_h", [(1e-3, 5e5), (1.0, 1e9), (0.5, -1e20), (2.0, 3e30)])
+def test_masked_columns_under_a_large_entropy_gradient(n, m, dtype, T, g_h):
+    g = torch.Generator().manual_seed(m)
+    row = (torch.randn(m, generator=g) * 2 * T).to(dtype)
+    row[::3] = NEG
+    row[1::3] = torch.finfo(dtype).min
+    token = 2
+    leaf = row.to(DEV).expand(n, -1).contiguous().requires_grad_(True)
+    r = tp.token_logprobs(leaf, torch.full((n,), token, device=DEV), temperature=T)
+    grad, = torch.autograd.grad((r.logprobs, r.entropy), leaf, (torch.full((n,), 1.5, device=DEV), torch.full((n,), g_h, device=DEV)))
+    w = ref.logprobs(row.double(), token, T, 0, 1.5, g_h)
+    if float(w["grad"].abs().max()) < torch.finfo(dtype).max:
+        ref.close(grad[0], w["grad"], w["grad_tol"], dtype)
+    assert torch.equal(grad, grad[:1].expand(n, -1))
+    masked = torch.ones(m, dtype=torch.bool)
+    masked[2::3] = False
+    assert int(torch.count_nonzero(grad[0].cpu()[masked])) == 0
