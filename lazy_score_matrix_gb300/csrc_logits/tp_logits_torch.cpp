@@ -476,6 +476,9 @@ std::tuple<Tensor, Tensor> distillation_grad_autograd(const Tensor& logits, cons
 void check_out(const Tensor& logits, const Tensor& out) {
     TORCH_CHECK_VALUE(out.sizes() == logits.sizes() && out.scalar_type() == logits.scalar_type() && out.device() == logits.device(),
                       "out must have the logits' shape, dtype and device");
+    // bump_version would say so too, but behind the write
+    TORCH_CHECK(!out.is_inference() || c10::InferenceMode::is_enabled(),
+                "out was made under inference mode and cannot be written outside of it");
 }
 Tensor distillation_grad_out_meta(const Tensor& logits, const Tensor& ids, const Tensor& values, const OptTensor& weights, double,
                                   bool, Tensor& out) {

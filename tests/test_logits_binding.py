@@ -1,5 +1,5 @@
 """What PyTorch's machinery around a call does with the stored-row consumers: tracing, forward-mode derivatives, function
-transforms, saved tensors that come back otherwise."""
+transforms, saved tensors that come back otherwise, inference mode."""
 import pytest
 import torch
 from torch.autograd import forward_ad
@@ -165,6 +165,18 @@ def test_negated_views():
     neg = torch.complex(torch.zeros_like(w), -w).conj().imag
     assert neg.is_neg() and torch.equal(neg, w)
     assert torch.equal(tp.topk_distillation_grad(x, ids, values, neg)[1], tp.topk_distillation_grad(x, ids, values, w)[1])
+
+
+def test_output_made_under_inference_mode():
+    x, tokens, ids, values, w = inputs(1)
+    want = tp.topk_distillation_grad(x, ids, values, w)[1]
+    with torch.inference_mode():
+        out = torch.full_like(x, 7.0)
+        assert torch.equal(tp.topk_distillation_grad(x, ids, values, w, out=out)[1], want)
+        out.fill_(7.0)
+    with pytest.raises(RuntimeError):  # as any write to it outside
+        tp.topk_distillation_grad(x, ids, values, w, out=out)
+    assert (out == 7.0).all()  # and nothing was written
 
 
 @pytest.mark.parametrize("n,m", [(3, 2), (5, 261), (4, 20011), (1300, 700)])
