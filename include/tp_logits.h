@@ -62,7 +62,8 @@ TP_API tp_status tp_token_logprobs(const tp_rows* logits, const int64_t* tokens,
  *     dL/dx_v = (grad_logprobs_i ([v = t] - p_v) - grad_entropy_i p_v (log p_v + entropy_i)) / T
  * logits, tokens, temperature as in the forward, stats as it wrote them; either upstream gradient [N] may
  * be NULL (zero), not both; masked columns get 0 as long as their values over T stay below 2^120. grad may be
- * the logits themselves (same data, type and strides: overwritten); otherwise it must not overlap an input. */
+ * the logits themselves (same data, type and strides: overwritten), or lie between their rows at the same
+ * strides (two halves of one buffer's rows); otherwise it must lie outside the span of every input. */
 TP_API tp_status tp_token_logprobs_backward(const tp_rows* logits, const int64_t* tokens, double temperature,
                                             const float* stats, const float* grad_logprobs,
                                             const float* grad_entropy, const tp_rows* grad, void* stream);

@@ -96,13 +96,37 @@ tp_status check_temperature(double t) {
     return TP_OK;
 }
 
+// Whether an offset at + k step, |k| < n, comes closer to 0 than `near` by way of f(at + k step); only the two k about
+// -at / step can, where step >= near.
+template <class F>
+bool near_zero(int64_t at, int64_t step, int64_t n, F f) {
+    if (n == 1) return f(at);
+    const int64_t k0 = -at / step - (-at % step < 0);
+    for (int64_t k = k0; k <= k0 + 1; ++k)
+        if (k > -n && k < n && f(at + k * step)) return true;
+    return false;
+}
+
+// Whether rows at the same strides, which do not overlap among themselves, share an element: a row of one then lies less
+// than M from a row of the other. The smaller stride's rows fill less than one step of the larger.
+bool share_elements(const tp_rows* x, const tp_rows* g) {
+    const int64_t at = (static_cast<const char*>(g->data) - static_cast<const char*>(x->data)) / (int64_t)rows_esize(x);
+    const int64_t groups = x->N / x->group;
+    const bool swap = x->group > 1 && groups > 1 && x->row_stride > x->group_stride;
+    const int64_t outer = swap ? x->row_stride : x->group_stride, inner = swap ? x->group_stride : x->row_stride;
+    return near_zero(at, outer, swap ? x->group : groups, [&](int64_t a) {
+        return near_zero(a, inner, swap ? groups : x->group, [&](int64_t b) { return b > -x->M && b < x->M; });
+    });
+}
+
 // grad: rows of the logits' type and shape; either the logits themselves or apart from them
 tp_status check_grad(const tp_rows* x, const tp_rows* g) {
     TP_CHECK(check_rows(g, "grad", true));
     if (g->dtype != x->dtype || g->N != x->N || g->M != x->M) return invalid("grad must have the logits' dtype, N and M");
-    const bool same = g->data == x->data && g->group == x->group && (g->group == 1 || g->row_stride == x->row_stride) &&
-                      (g->group == g->N || g->group_stride == x->group_stride);
-    if (!same && overlap({x->data, rows_extent(x), ""}, {g->data, rows_extent(g), ""}))
+    const bool alike = g->group == x->group && (g->group == 1 || g->row_stride == x->row_stride) &&
+                       (g->group == g->N || g->group_stride == x->group_stride);
+    if (alike && g->data == x->data) return TP_OK;
+    if (overlap({x->data, rows_extent(x), ""}, {g->data, rows_extent(g), ""}) && (!alike || share_elements(x, g)))
         return invalid("grad overlaps the logits without being the same rows");
     return TP_OK;
 }

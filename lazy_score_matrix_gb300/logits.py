@@ -74,5 +74,6 @@ def topk_distillation_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teac
     (a mask over the number of tokens, a loss scale; all ones when None). The loss is not weighted. Each row
     comes from memory once for both, so this is the form for training: ``logits.backward(gradient)``.
 
-    out: where the gradient is written; it may be the logits themselves, which are then overwritten."""
+    out: where the gradient is written; it may be the logits themselves, which are then overwritten, or lie between
+    their rows at the same strides (``buffer[:, M:]`` for logits ``buffer[:, :M]``)."""
     return _lib.logits_binding().topk_distillation_grad(logits, teacher_ids, teacher_values, weights, temperature, rest, out)
