@@ -3,7 +3,8 @@ _tp_logits.so, the PyTorch binding of include/tp_logits.h (csrc_logits/tp_logits
 
 Usage: ``python -m lazy_score_matrix_gb300.build`` (or ``__graft_entry__.build()``).
 Objects go to ``lazy_score_matrix_gb300/_build/``; the library to ``lazy_score_matrix_gb300/libtp.so``.
-A translation unit is recompiled when it or any header in csrc/, csrc_logits/ or include/ is newer than its object.
+A translation unit is recompiled when it or any header in csrc/, csrc_logits/ or include/ is newer than its object; the
+binding also when its object was made for another PyTorch or Python.
 
 csrc/ holds the consumers of lazy scores (include/tp.h), csrc_logits/ those of stored score rows
 (include/tp_logits.h). They are apart because the recorded traffic and instruction counts of the lazy
@@ -65,12 +66,29 @@ def _torch_dirs() -> tuple[list[str], str]:
     return [inc, os.path.join(inc, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"], cuda], os.path.join(torch, "lib")
 
 
+def _binding_key() -> str:
+    """What the binding was compiled against: an object for another PyTorch or Python is not reused."""
+    import importlib.util
+    spec = os.path.dirname(importlib.util.find_spec("torch").origin)
+    return f"{sys.version}\n{spec}\n{open(os.path.join(spec, 'version.py')).read()}"
+
+
+def _binding_due() -> bool:
+    obj, key = os.path.join(OBJ_DIR, "tp_logits_torch.o"), os.path.join(OBJ_DIR, "tp_logits_torch.key")
+    if not os.path.exists(obj) or not os.path.exists(key) or open(key).read() != _binding_key():
+        return True
+    return os.path.getmtime(obj) < max(os.path.getmtime(f) for f in [BINDING_SRC, *glob.glob(os.path.join(INCLUDE, "*.h"))])
+
+
 def _compile_binding() -> tuple[str, int, str]:
     obj = os.path.join(OBJ_DIR, "tp_logits_torch.o")
     incs, _ = _torch_dirs()
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden", "-DTORCH_API_INCLUDE_EXTENSION_H",
            "-I" + INCLUDE, *[a for d in incs for a in ("-isystem", d)], "-c", BINDING_SRC, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode == 0:
+        with open(os.path.join(OBJ_DIR, "tp_logits_torch.key"), "w") as f:
+            f.write(_binding_key())
     return obj, r.returncode, (r.stdout + r.stderr)
 
 
@@ -95,8 +113,7 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False, e
         if force or not os.path.exists(obj) or os.path.getmtime(obj) < max(os.path.getmtime(s), hdr):
             todo.append(s)
     bound = os.path.join(OBJ_DIR, "tp_logits_torch.o")
-    bind = force or not os.path.exists(bound) or os.path.getmtime(bound) < max(
-        os.path.getmtime(BINDING_SRC), *(os.path.getmtime(h) for h in glob.glob(os.path.join(INCLUDE, "*.h"))))
+    bind = force or _binding_due()
     jobs = jobs or max(1, min(len(todo) + bind or 1, os.cpu_count() or 4))
     errors = []
     if todo or bind:
