@@ -2,8 +2,8 @@
 // near zero is the difference of logarithms that agree to several digits, which one fp32 word does not hold,
 // and fp64 has two lanes a clock per SM here: a warp's dozen fp64 exponentials and logarithms took longer than
 // a row's reduction. exp and ln are the table-driven methods of P. T. P. Tang (ACM Trans. Math. Softw. 15(2),
-// 1989; 16(4), 1990) with the leading terms in two words; their absolute (ln) and relative (exp) errors are
-// about 2e-9.
+// 1989; 16(4), 1990) with the leading terms in two words; errors at most 2.2e-9 (exp, relative; from e^-70 down
+// its second word falls under fp32's smallest step, 6e-8 at the worst) and 3.7e-9 (ln, absolute).
 #pragma once
 
 #include <cuda_runtime.h>
