@@ -158,11 +158,12 @@ using below_autograd = at::AutoDispatchBelowADInplaceOrView;
 // profiler that wants to see operators. It then runs that function directly: the dispatcher's two passes add 0.3 us to the 2.1 that a call
 // takes on a Grace core without its launch, and with the launch behind them 1 to 2, a third of a short row's kernel.
 template <class... T>
-bool plain(const T&... tensors) {
+bool plain(const T&... tensors) {  // undefined ones do not count
     constexpr auto ordinary = c10::DispatchKeySet({c10::DispatchKey::Dense, c10::DispatchKey::BackendSelect, c10::DispatchKey::ADInplaceOrView}) |
                               c10::autograd_dispatch_keyset | c10::autocast_dispatch_keyset;
     auto keys = c10::impl::tls_local_dispatch_key_set().included_;
     const auto add = [&](const Tensor& t) {
+        if (!t.defined()) return true;
         keys = keys | t.key_set();
         return t.is_cuda() && !tangent(t);
     };
@@ -258,12 +259,13 @@ struct LogprobsFn : torch::autograd::Function<LogprobsFn> {
     static variable_list forward(torch::autograd::AutogradContext* ctx, const Tensor& logits, const OptTensor& tokens,
                                  double temperature, int64_t top) {
         const below_autograd guard;
-        const Tensor x = readable(logits);
-        auto out = logprobs_op(x, tokens, temperature, top, true);
+        const Tensor x = readable(logits), t = tokens ? *tokens : Tensor();
+        auto out = plain(x, t) ? logprobs_cuda(x, tokens, temperature, top, true) : logprobs_op(x, tokens, temperature, top, true);
         ctx->set_materialize_grads(false);
-        ctx->save_for_backward({x, tokens ? *tokens : Tensor(), out.back()});
+        ctx->save_for_backward({x, t, out.back()});
+        out.pop_back();
         ctx->saved_data["T"] = temperature;
-        ctx->mark_non_differentiable({out.end() - (top ? 3 : 1), out.end()});
+        if (top) ctx->mark_non_differentiable({out.end() - 2, out.end()});
         return out;
     }
     static variable_list backward(torch::autograd::AutogradContext* ctx, const variable_list& grads) {
@@ -273,7 +275,8 @@ struct LogprobsFn : torch::autograd::Function<LogprobsFn> {
         if (!g_h.defined() && !g_lp.defined()) return {Tensor(), Tensor(), Tensor(), Tensor()};
         const auto grad = [&] {
             const below_autograd guard;
-            return logprobs_backward_op(saved[0], maybe(tokens), ctx->saved_data["T"].toDouble(), saved[2], maybe(g_lp), maybe(g_h));
+            const auto call = plain(saved[0], tokens, saved[2], g_lp, g_h) ? logprobs_backward_cuda : logprobs_backward_op;
+            return call(saved[0], maybe(tokens), ctx->saved_data["T"].toDouble(), saved[2], maybe(g_lp), maybe(g_h));
         };
         return {once(grad()), Tensor(), Tensor(), Tensor()};
     }
@@ -283,9 +286,8 @@ std::vector<Tensor> logprobs_autograd(const Tensor& logits, const OptTensor& tok
     refuse_tangents("token_logprobs", logits);
     if (wants_grad(logits)) {
         check_rows_type(logits, "logits");
-        auto out = LogprobsFn::apply(logits, maybe(side(tokens_, at::kLong, "tokens", lead_of(logits), logits)), temperature, top);
-        if (!stats) out.pop_back();
-        return out;
+        TORCH_CHECK(!stats, "token_logprobs: the statistics are for the backward, which autograd calls here");
+        return LogprobsFn::apply(logits, maybe(side(tokens_, at::kLong, "tokens", lead_of(logits), logits)), temperature, top);
     }
     const below_autograd guard;
     return logprobs_op(logits, tokens_, temperature, top, stats);
@@ -295,11 +297,12 @@ using Four = std::tuple<OptTensor, Tensor, OptTensor, OptTensor>;
 
 Four token_logprobs(const Tensor& logits, const OptTensor& tokens, double temperature, int64_t top) {
     check_device(logits);
-    if (!wants_grad(logits) && (tokens ? plain(logits, *tokens) : plain(logits))) {
+    const bool direct = tokens ? plain(logits, *tokens) : plain(logits);
+    if (direct && !wants_grad(logits)) {
         const Logprobs o = logprobs_forward(logits, tokens, temperature, top, false);
         return {maybe(o.logprobs), o.entropy, maybe(o.top_logprobs), maybe(o.top_ids)};
     }
-    const auto out = logprobs_op(logits, tokens, temperature, top, false);
+    const auto out = (direct ? logprobs_autograd : logprobs_op)(logits, tokens, temperature, top, false);
     const size_t at = tokens ? 2 : 1;
     return {tokens ? OptTensor(out[1]) : std::nullopt, out[0], top ? OptTensor(out[at]) : std::nullopt,
             top ? OptTensor(out[at + 1]) : std::nullopt};
@@ -386,26 +389,23 @@ Tensor distillation_backward_op(const Tensor& logits, const Tensor& ids, const T
 }
 
 struct DistillationFn : torch::autograd::Function<DistillationFn> {
-    static variable_list forward(torch::autograd::AutogradContext* ctx, const Tensor& logits, const Tensor& ids, const Tensor& values,
-                                 double temperature, bool rest) {
+    static Tensor forward(torch::autograd::AutogradContext* ctx, const Tensor& logits, const Tensor& ids, const Tensor& values,
+                          double temperature, bool rest) {
         const below_autograd guard;
         const Tensor x = readable(logits);
-        auto out = distillation_op(x, ids, values, temperature, rest, true);
-        ctx->set_materialize_grads(false);
+        const auto out = (plain(x, ids, values) ? distillation_cuda : distillation_op)(x, ids, values, temperature, rest, true);
         ctx->save_for_backward({x, ids, values, out[1]});
         ctx->saved_data["T"] = temperature;
         ctx->saved_data["rest"] = rest;
-        ctx->mark_non_differentiable({out[1]});
-        return out;
+        return out[0];
     }
     static variable_list backward(torch::autograd::AutogradContext* ctx, const variable_list& grads) {
         const auto saved = ctx->get_saved_variables();
         refuse_tangents("topk_distillation", grads[0]);
-        if (!grads[0].defined()) return {Tensor(), Tensor(), Tensor(), Tensor(), Tensor()};
         const auto grad = [&] {
             const below_autograd guard;
-            return distillation_backward_op(saved[0], saved[1], saved[2], ctx->saved_data["T"].toDouble(), ctx->saved_data["rest"].toBool(),
-                                            saved[3], grads[0]);
+            const auto call = plain(saved[0], saved[1], saved[2], saved[3], grads[0]) ? distillation_backward_cuda : distillation_backward_op;
+            return call(saved[0], saved[1], saved[2], ctx->saved_data["T"].toDouble(), ctx->saved_data["rest"].toBool(), saved[3], grads[0]);
         };
         return {once(grad()), Tensor(), Tensor(), Tensor(), Tensor()};
     }
@@ -418,9 +418,8 @@ std::vector<Tensor> distillation_autograd(const Tensor& logits, const Tensor& id
     if (wants_grad(logits)) {
         check_rows_type(logits, "logits");
         const Teacher y = teacher_of(ids, values, logits);
-        auto out = DistillationFn::apply(logits, y.ids, y.values, temperature, rest);
-        if (!stats) out.pop_back();
-        return out;
+        TORCH_CHECK(!stats, "topk_distillation: the statistics are for the backward, which autograd calls here");
+        return {DistillationFn::apply(logits, y.ids, y.values, temperature, rest)};
     }
     const below_autograd guard;
     return distillation_op(logits, ids, values, temperature, rest, stats);
@@ -428,9 +427,9 @@ std::vector<Tensor> distillation_autograd(const Tensor& logits, const Tensor& id
 
 Tensor topk_distillation(const Tensor& logits, const Tensor& ids, const Tensor& values, double temperature, bool rest) {
     check_device(logits);
-    if (!wants_grad(logits) && !wants_grad(values) && plain(logits, ids, values))
-        return distillation_forward(logits, ids, values, temperature, rest, false).loss;
-    return distillation_op(logits, ids, values, temperature, rest, false)[0];
+    const bool direct = plain(logits, ids, values);
+    if (direct && !wants_grad(logits) && !wants_grad(values)) return distillation_forward(logits, ids, values, temperature, rest, false).loss;
+    return (direct ? distillation_autograd : distillation_op)(logits, ids, values, temperature, rest, false)[0];
 }
 
 // The loss, and its gradient into `grad` (rows g).
