@@ -2,6 +2,7 @@
 transforms, saved tensors that come back otherwise, inference mode."""
 import pytest
 import torch
+import torch.utils.checkpoint
 from torch.autograd import forward_ad
 from torch.fx.experimental.proxy_tensor import make_fx
 
@@ -192,3 +193,62 @@ def test_entropy_and_its_gradient_without_tokens(n, m, dtype, top):
     assert r.logprobs is None and torch.equal(r.entropy, w.entropy)
     grads = [torch.autograd.grad(o.entropy.sum(), leaf)[0] for o, leaf in zip((r, w), leaves)]
     assert torch.equal(*grads)
+
+
+def whole_step(x, *rest):
+    leaf = x.detach().requires_grad_(True)
+    loss = differentiable(leaf, *rest) - 0.2 * tp.token_logprobs(leaf).entropy.mean()
+    loss.backward()
+    return [loss.detach(), leaf.grad, *no_grad_calls(x, *rest)]
+
+
+def under_profiler(args):
+    with torch.profiler.profile(activities=[torch.profiler.ProfilerActivity.CPU]) as p:
+        got = whole_step(*args)
+    assert {"lazy_score_matrix_gb300::token_logprobs", "lazy_score_matrix_gb300::topk_distillation_grad"} <= {e.name for e in p.events()}
+    return got
+
+
+def under_checkpoint(args):
+    x, *rest = args
+    leaf = x.detach().requires_grad_(True)
+    loss = torch.utils.checkpoint.checkpoint(lambda t: differentiable(t, *rest) - 0.2 * tp.token_logprobs(t).entropy.mean(), leaf, use_reentrant=False)
+    loss.backward()
+    return [loss.detach(), leaf.grad, *no_grad_calls(*args)]
+
+
+def under(manager):
+    def run(args):
+        with manager():
+            return whole_step(*args)
+    return run
+
+
+def on_another_thread(args):
+    import threading
+    got = []
+    t = threading.Thread(target=lambda: got.extend(whole_step(*args)))
+    t.start()
+    t.join()
+    return got
+
+
+TOOLS = {"profiler": under_profiler, "checkpoint": under_checkpoint, "anomaly mode": under(lambda: torch.autograd.set_detect_anomaly(True)),
+         "autocast": under(lambda: torch.autocast("cuda", dtype=torch.bfloat16)), "saved on the CPU": under(torch.autograd.graph.save_on_cpu),
+         "another thread": on_another_thread}
+
+
+@pytest.mark.parametrize("tool", TOOLS)
+def test_the_same_results_under_pytorch_tools(tool):
+    args = inputs(4, dtype=torch.bfloat16)
+    want, got = whole_step(*args), TOOLS[tool](args)
+    assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_a_gradient_traced_without_data():
+    def step(x, *rest):
+        y = x.detach().requires_grad_(True)
+        return torch.autograd.grad(differentiable(y, *rest), y)[0]
+
+    traced = make_fx(step, tracing_mode="fake")(*inputs(1))
+    assert torch.equal(traced(*inputs(2)), step(*inputs(2)))
