@@ -19,9 +19,12 @@
  *     alone has log probability -inf, entropy 0, no alternatives and gradient 0. The type's lowest value is a
  *     score like any other, at any temperature: its probability is 0 beside an ordinary one, its distance
  *     finite. NaN or +inf in a row that is read gives NaN in its results; nothing else is promised for them.
- *   - Rows left out (a token, or a whole list, that does not count) are not read: zeros, (-inf, -1), and a
- *     zero gradient, whatever the row holds.
- *   - Results do not depend on the run: no atomics on floating data, the same call gives the same bits.
+ *   - Rows left out (a token, or a whole list, that does not count) are not looked at: zeros, (-inf, -1), and
+ *     a zero gradient, whatever the row holds. (Their memory must be there all the same: a row's first scores
+ *     may be on their way to the cache before its token or list is seen.)
+ *   - Results do not depend on the run: no atomics on floating data, the same call gives the same bits. Another
+ *     number of rows or alternatives, or another alignment, may split a row over other threads, and its sums
+ *     then round otherwise in the last bits.
  */
 #ifndef TP_LOGITS_H_
 #define TP_LOGITS_H_

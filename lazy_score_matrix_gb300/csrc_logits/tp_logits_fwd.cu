@@ -463,7 +463,11 @@ template <class T>
 void run_logprobs(LogprobArgs a, cudaStream_t s) {
     HookScope h("token_logprobs", s);
     const int64_t row = (int64_t)a.x.M * (int64_t)sizeof(T);
-    const bool large = a.top && a.N < kResident;  // few rows with alternatives: CTAs of kLongThreads
+    // Up to 32 alternatives for a warp a row: its 32 maxima bound no more than the 32nd largest score. Few rows with
+    // alternatives: CTAs of kLongThreads, which alone come in clusters there. Against a CTA of 256 a row, cold: 1 x 131072 bf16,
+    // 5 alternatives, 15 us and 17; 8 rows 15 and 19; 64 rows 18 and 19. Where a cluster is small or the row short they lose: 64
+    // alternatives, 128 x 131072 24 and 21 us, 600 x 65536 36 and 30; 5 alternatives, 600 x 4096 21 and 12.
+    const bool large = a.top && a.N < kResident;
     Shape sh = shape_of(a.N, row, a.top <= 32 ? kWarpBytes : 0, large ? kResidentLong : kResident);
     a.under_way = kResident;
     if (a.x.M <= kShort && a.top <= 32) {

@@ -56,10 +56,10 @@ __global__ void __launch_bounds__(TEAM == 32 ? kThreads : TEAM, TEAM == kLongThr
     Fetch<T, TEAM, false> scores(o, e0, e1, from);  // the second reading begins while the states meet
     st = team_state<TEAM>(st, a.sc.c, red);
     if (size > 1) {
-        cluster_wait();  // every CTA of the cluster runs, and has looked the listed scores up
+        cluster_wait();  // every CTA of the cluster runs
         cluster_share(st, parts, rank, size);
         cluster_arrive();
-        cluster_wait();
+        cluster_wait();  // every CTA has looked the listed scores up: from here on the row may be overwritten
         st = cluster_merge(parts, size, a.sc.c);
     }
     RowStats s;
@@ -85,8 +85,11 @@ __global__ void __launch_bounds__(TEAM == 32 ? kThreads : TEAM, TEAM == kLongThr
     distill_list_grad<T, TEAM>(a, s, w, o, e0, e1, list, twice);
 }
 
-// Where the CTAs that an SM's registers admit would have more rows under way than the cache keeps, one is kept alone on
-// its SM by shared memory that it does not use.
+// CTAs of 256 have 608 rows under way, of 512 304; where those would be more than the cache keeps, one of 512 is kept alone
+// on its SM by shared memory that it does not use. 3000 rows bf16, 33 entries, CTAs of 256 and of 512: 65536 columns 146 and 170 us,
+// 90112 (608 rows are 110 MB) 216 and 211, 131072 341 and 285. 1000 rows, 64 entries, two on an SM and one alone: bf16
+// 180224 columns (304 rows are 110 MB) 162 and 169 us, 262144 242 and 234, 700000 669 and 683; fp32 200000 374 and 357, 524288 986
+// and 980. Alone gains from 304 rows on; with fewer the second place on an SM is worth more (200 x 262144: 56 and 67).
 constexpr int64_t kCacheBytes = (int64_t)110 << 20;
 constexpr size_t kAlone = 120 * 1024;
 

@@ -12,6 +12,8 @@ such lists: a student's rows against the top columns of a teacher's. Both read e
 Logits are float32, float16 or bfloat16 CUDA tensors of any leading shape; rows may lie at any stride (a slice of
 a padded vocabulary, ``logits[:, :-1]`` of a batch) and are copied only when two strides cannot describe them.
 Results are float32, gradients have the logits' type. Columns at -inf are masked: probability 0, never chosen.
+The same call gives the same bits; a row by itself and the same row in a batch may differ in the last ones, as its
+sums are split over other threads.
 
 The calls are operators of PyTorch's dispatcher: a trace (``torch.jit.trace``, ``make_fx``) holds them, runs them again
 on its own inputs and has their gradients. (A trace saved to a file needs ``_lib.logits_binding()`` before it is
@@ -41,7 +43,7 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     [..., top]), natural logarithms; logprobs is None without tokens, the top fields are None for top = 0.
 
     Alternatives descend by logit, ties by ascending column; a row with fewer than ``top`` (at most 128) columns
-    above -inf ends in (-inf, -1). A token outside [0, M), such as -1 or -100, leaves its row out: it is not read
+    above -inf ends in (-inf, -1). A token outside [0, M), such as -1 or -100, leaves its row out: it is not looked at
     and gives zeros, (-inf, -1) and a zero gradient. A row of -inf alone has log probability -inf and entropy 0.
 
     Differentiable in logprobs and entropy; the alternatives carry no gradient. temperature in [1e-3, 1e3]."""
@@ -61,7 +63,7 @@ def topk_distillation(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_v
         loss = sum_k q_k (log q_k - log p_k)  [+ q_r (log q_r - log p_r)]      p = softmax(logits / temperature)
 
     An id outside [0, M) or a value of -inf drops the entry (a shorter list); a row without an entry is left out:
-    not read, loss 0, gradient 0. A column listed twice holds both shares. Differentiable in the logits; the
+    not looked at, loss 0, gradient 0. A column listed twice holds both shares. Differentiable in the logits; the
     teacher's list is a constant. Multiply by temperature ** 2 to keep gradients of different temperatures in
     proportion."""
     return _lib.logits_binding().topk_distillation(logits, teacher_ids, teacher_values, temperature, rest)
