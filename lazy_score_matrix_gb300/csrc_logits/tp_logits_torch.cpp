@@ -131,9 +131,9 @@ OptTensor maybe(const Tensor& t) { return t.defined() ? OptTensor(t) : std::null
 
 // --- operators ---------------------------------------------------------------------------------------------------
 //
-// Calls go through PyTorch's dispatcher as operators with a schema, so that whatever records calls (jit.trace, make_fx) records
-// them, runs them again on replay and finds their gradients there, and fake tensors get shapes. Outside the dispatcher a
-// trace would hold nothing of a call but the allocation of its outputs.
+// Calls go through PyTorch's dispatcher as operators with a schema, so that whatever records calls (jit.trace, make_fx)
+// records them, runs them again on replay and finds their gradients there, and fake tensors get shapes. Outside the
+// dispatcher a trace would hold nothing of a call but the allocation of its outputs.
 //
 //   CUDA      allocates the outputs and calls libtp
 //   Meta      the outputs' shapes and types
@@ -141,7 +141,8 @@ OptTensor maybe(const Tensor& t) { return t.defined() ? OptTensor(t) : std::null
 
 template <class F>
 auto op_of(const char* name) {
-    return c10::Dispatcher::singleton().findSchemaOrThrow((std::string("lazy_score_matrix_gb300::") + name).c_str(), "").template typed<F>();
+    const std::string full = std::string("lazy_score_matrix_gb300::") + name;
+    return c10::Dispatcher::singleton().findSchemaOrThrow(full.c_str(), "").template typed<F>();
 }
 
 // No forward-mode derivatives, as the lazy consumers have none: a tangent is refused, not dropped.
@@ -155,12 +156,14 @@ void refuse_tangents(const char* where, const T&... tensors) {
 using below_autograd = at::AutoDispatchBelowADInplaceOrView;
 
 // Whether a call on these tensors is the CUDA function's alone: no subclass, mode, trace or transform, no tangent, no
-// profiler that wants to see operators. It then runs that function directly: the dispatcher's two passes add 0.3 us to the 2.1 that a call
-// takes on a Grace core without its launch, and with the launch behind them 1 to 2, a third of a short row's kernel.
+// profiler that wants to see operators. (Undefined tensors do not count.) It then runs that function directly: the
+// dispatcher's two passes add 0.3 us to the 2.1 that a call takes on a Grace core without its launch, and with the launch
+// behind them 1 to 2, a third of a short row's kernel; to a call and its gradient by autograd, 8 us.
 template <class... T>
-bool plain(const T&... tensors) {  // undefined ones do not count
-    constexpr auto ordinary = c10::DispatchKeySet({c10::DispatchKey::Dense, c10::DispatchKey::BackendSelect, c10::DispatchKey::ADInplaceOrView}) |
-                              c10::autograd_dispatch_keyset | c10::autocast_dispatch_keyset;
+bool plain(const T&... tensors) {
+    constexpr auto ordinary =
+        c10::DispatchKeySet({c10::DispatchKey::Dense, c10::DispatchKey::BackendSelect, c10::DispatchKey::ADInplaceOrView}) |
+        c10::autograd_dispatch_keyset | c10::autocast_dispatch_keyset;
     auto keys = c10::impl::tls_local_dispatch_key_set().included_;
     const auto add = [&](const Tensor& t) {
         if (!t.defined()) return true;
@@ -168,7 +171,8 @@ bool plain(const T&... tensors) {  // undefined ones do not count
         return t.is_cuda() && !tangent(t);
     };
     const bool cuda = (add(tensors) && ...);
-    return cuda && !(keys.raw_repr() & ~ordinary.raw_repr() & ~c10::full_backend_mask) && !at::getStepCallbacksUnlessEmpty(at::RecordScope::FUNCTION);
+    return cuda && !(keys.raw_repr() & ~ordinary.raw_repr() & ~c10::full_backend_mask) &&
+           !at::getStepCallbacksUnlessEmpty(at::RecordScope::FUNCTION);
 }
 bool wants_grad(const Tensor& t) { return at::GradMode::is_enabled() && t.requires_grad(); }
 

@@ -6,6 +6,7 @@ import torch
 
 import lazy_score_matrix_gb300 as tp
 from lazy_score_matrix_gb300 import _lib
+from lazy_score_matrix_gb300 import build as tpbuild
 from tests.test_logits import scores, teacher_list
 
 DEV = "cuda"
@@ -19,6 +20,7 @@ def elements(at, n, m, group, rs, gs):
 
 def test_rows_between_rows_are_told_from_rows_on_rows(monkeypatch):
     # every accepted pair shares no element or all of them, every refused one shares some; against sets of elements
+    tpbuild.build()
     lib = _lib.load()
     monkeypatch.setenv("TP_FAULT_INJECT", "topk_distillation_grad")  # what is accepted ends in the injected fault
     rng = random.Random(3)
