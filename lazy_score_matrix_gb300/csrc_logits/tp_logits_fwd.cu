@@ -192,6 +192,9 @@ __device__ __forceinline__ void leave_out(const LogprobArgs& a, int64_t row, int
     for (int i = t; i < a.top; i += team) a.top_logprobs[row * a.top + i] = neg_inf(), a.top_ids[row * a.top + i] = -1;
 }
 
+// (x - m)/T where the difference itself may leave fp32's range; the bits of (x - m) inv elsewhere
+__device__ __forceinline__ float scaled_distance(float x, float m, float inv) { return (0.5f * x - 0.5f * m) * (2.f * inv); }
+
 // The row's results from its state, the token's score xt (thread 0) and the keys of its best columns; `shared`: a word
 // for the CTA.
 template <int TEAM, bool TOP>
@@ -204,7 +207,7 @@ __device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, con
         if (TOP && TEAM != 32) *shared = ls;  // to the other warps
         const float H = some ? ls - st.h / z * a.sc.inv : 0.f;
         a.entropy[row] = H;
-        if (a.logprobs) a.logprobs[row] = some ? (xt - st.m) * a.sc.inv - ls : neg_inf();
+        if (a.logprobs) a.logprobs[row] = some ? scaled_distance(xt, st.m, a.sc.inv) - ls : neg_inf();
         if (a.stats) {
             float* o = a.stats + row * kStats;
             o[0] = st.m, o[1] = ls, o[2] = H;
@@ -226,7 +229,7 @@ __device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, con
                 place += (p.x > k) + (p.y > k);
             }
             if (place < a.top) {
-                a.top_logprobs[row * a.top + place] = (of_ord((uint32_t)(k >> 32)) - st.m) * a.sc.inv - ls;
+                a.top_logprobs[row * a.top + place] = scaled_distance(of_ord((uint32_t)(k >> 32)), st.m, a.sc.inv) - ls;
                 a.top_ids[row * a.top + place] = (int64_t)(~(uint32_t)k);
             }
         }

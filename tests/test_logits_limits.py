@@ -83,6 +83,22 @@ def test_a_distance_beyond_the_range(T):
     check_list(row, [20, 9], [0.01, 0.99], T, False, 2)
 
 
+@pytest.mark.parametrize("n,m", SHAPES)
+@pytest.mark.parametrize("T", [0.5, 0.9, 1.0, 3.0])
+def test_log_probabilities_beyond_the_range_of_a_difference(n, m, T):
+    row = torch.full((m,), -3e38)
+    row[9], row[20], row[21] = 3e38, -1e38, NEG
+    tokens = torch.tensor([9, 20, 5, 21], device=DEV).repeat(n)[:n]
+    r = tp.token_logprobs(row.to(DEV).expand(n, m).contiguous(), tokens, temperature=T, top=7)
+    big = 2.0 ** 128 * (1 - 2.0 ** -25)
+    for i in range(min(n, 4)):
+        w = ref.logprobs(row.double(), int(tokens[i]), T, 7)
+        out = lambda v: NEG if v <= -big else v  # noqa: E731
+        ref.close(r.logprobs[i], out(w["lp"]), w["lp_tol"])
+        ref.close(r.top_logprobs[i], [out(v) for v in w["top_lp"]], w["top_tol"])
+        assert r.top_ids[i].tolist() == w["top_ids"] and r.entropy[i] == 0
+
+
 @pytest.mark.parametrize("rest", [False, True])
 def test_infinite_and_nan_scores_still_show(rest):
     x = torch.full((4, 600), torch.finfo(torch.float32).min, device=DEV)
